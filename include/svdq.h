@@ -214,6 +214,129 @@ svdq_status svdq_kv_attention(const void* Q, int32_t Mq, const uint8_t* kcodes, 
                               int64_t T, int32_t C, int32_t heads, int32_t dtype, float* out, void* workspace,
                               size_t ws_bytes, svdq_stream stream);
 
+/* ------------------------------------------------- paged 8-bit KV cache
+ * A KV cache for many requests at once (the serving form of the INT8 cache
+ * above; "VAR-Compressor：在边缘GPU上实现80亿参数视觉自回归模型的高效量化部署",
+ * INT8 KV缓存量化).  A pool of n_blocks blocks holds `block_size` tokens each:
+ *   kcodes, vcodes  n_blocks x kv_heads x block_size x head_dim, one byte a value
+ *   kscale, vscale  n_blocks x kv_heads fp32
+ * so that a key or value is code * scale, with one scale for a block's tokens
+ * of a head.  Codes are int8 in [-127, 127] (SVDQ_KV_INT8) or E4M3
+ * (SVDQ_KV_E4M3, |code| <= 448).  Request i's token t sits in block
+ * table[i][t / block_size], row t % block_size.
+ *
+ * One step of a server:
+ *   svdq_paged_plan       request lengths -> blocks, starts and slots
+ *   svdq_paged_append     the step's keys and values -> codes and scales
+ *   svdq_paged_attention  queries over the cache
+ * All three are asynchronous on `stream`, read lengths and tables on the
+ * device, and take host numbers only as upper bounds, so a step can be
+ * captured in a CUDA graph and replayed with other lengths.
+ *
+ * Limits: head_dim 64 or 128, block_size 16, 32, 64 or 128 (else
+ * SVDQ_ERR_UNSUPPORTED); heads a multiple of kv_heads (heads h G .. h G + G - 1
+ * read kv head h, G = heads / kv_heads); B <= 16384; n_blocks * block_size,
+ * B * max_blocks and max_blocks * block_size below 2^31.  Device pointers
+ * 16-byte aligned unless said otherwise.
+ */
+typedef enum { SVDQ_KV_INT8 = 1, SVDQ_KV_E4M3 = 2 } svdq_kv_format;
+
+/* The pool.  The caller owns the buffers; the struct is read during calls only. */
+typedef struct svdq_paged_cache {
+  uint8_t* kcodes;
+  float* kscale;
+  uint8_t* vcodes;
+  float* vscale;
+  int32_t heads;       /* query heads                          */
+  int32_t kv_heads;    /* key / value heads                    */
+  int32_t head_dim;
+  int32_t block_size;
+  int32_t n_blocks;
+  int32_t fmt;         /* svdq_kv_format                       */
+  int32_t dtype;       /* svdq_dtype of K, V, Q and the output */
+  int32_t reserved;    /* must be 0                            */
+} svdq_paged_cache;
+
+/* One step's requests.  New tokens are packed: request i's are rows
+ * cu[i] .. cu[i + 1] - 1 of K, V, Q and the output.  Device int32 arrays, 4-byte aligned. */
+typedef struct svdq_paged_batch {
+  int32_t* table;      /* B x max_blocks block numbers                          */
+  int32_t* lens;       /* B cached lengths, this step's tokens included         */
+  int32_t* cu;         /* B + 1 starts of the requests' new tokens              */
+  int32_t* slots;      /* n_tokens: block * block_size + row, -1: not a token   */
+  int32_t B;
+  int32_t max_blocks;
+  int32_t n_tokens;    /* rows of K, V, Q and the output (may exceed cu[B])     */
+  int32_t max_new;     /* no request has more new tokens than this              */
+  int32_t max_len;     /* nor a cached length above this (<= max_blocks * block_size) */
+  int32_t reserved;    /* must be 0                                             */
+} svdq_paged_batch;
+
+/*
+ * The plan of a step: request i's cached length goes from prev[i] to target[i]
+ * (device, B int32 each).  Growing takes blocks off the front of the ring of
+ * free block numbers (in request order), shrinking or ending (target 0) gives
+ * the blocks above ceil(target / block_size) back to its end.
+ *   ring       n_blocks int32; the free ones are ring[(head + k) % n_blocks],
+ *              k < count.  Start: 0 .. n_blocks - 1, head 0, count n_blocks.
+ *   state_in   {head, count, -, -};  state_out  {head, count, lacking, new
+ *              tokens}: 4 int32 each, device, two different buffers.
+ * Writes b->table (entries of new blocks; others stay as they are), b->lens =
+ * target, b->cu, b->slots (-1 from cu[B] to n_tokens) and the ring entries given
+ * back.  prev must not be b->lens: keep two length arrays and swap them, as with
+ * the states.  Nothing read is overwritten, so the same call made twice gives the
+ * same result.  Blocks given back are available to the next call.
+ * Refused as a whole, when the ring lacks blocks (lacking = how many) or the
+ * lengths are bad (lacking = -1: negative, above max_len, more than max_new new
+ * for one request or n_tokens for all, head or count outside the ring): no
+ * block moves, b->lens = prev, b->cu = 0, b->slots = -1.
+ * One kernel.  Errors: SVDQ_ERR_INVALID_ARG, SVDQ_ERR_UNSUPPORTED, SVDQ_ERR_CUDA.
+ */
+svdq_status svdq_paged_plan(const svdq_paged_batch* b, int32_t block_size, int32_t n_blocks, const int32_t* prev,
+                            const int32_t* target, int32_t* ring, const int32_t* state_in, int32_t* state_out,
+                            svdq_stream stream);
+
+/*
+ * Writes the step's keys and values into the cache.  K, V: n_tokens rows of
+ * kv_heads x head_dim values, dtype; k_stride, v_stride: elements between
+ * rows (multiples of 8), so views of a fused projection's output do.
+ * For a block and head, with x the block's new tokens, fp32, round to nearest even:
+ *   s = max(s_old, max |x| / qmax)   (qmax 127 or 448; s_old = 0 in a block
+ *                                     whose first row is new)
+ *   code = round(x / s);  earlier rows, when s grew: code = round(code (s_old / s)).
+ * A block of zeros has s = 0.  Inputs finite.
+ * Slots: those of one request follow one another within a block, as the plan
+ * writes them, and a block takes the new tokens of one request; a token whose
+ * slot is -1, or not next to the previous one in its block, is left out.  A slot
+ * past the pool is skipped and recorded for svdq_get_status (SVDQ_ERR_INVALID_ARG).
+ * One kernel.  Errors: SVDQ_ERR_INVALID_ARG, SVDQ_ERR_ALIGNMENT,
+ * SVDQ_ERR_UNSUPPORTED, SVDQ_ERR_CUDA.
+ */
+svdq_status svdq_paged_append(const svdq_paged_cache* c, const svdq_paged_batch* b, const void* K, int64_t k_stride,
+                              const void* V, int64_t v_stride, svdq_stream stream);
+
+/*
+ * Attention of the step's queries over the cache.  For new token j of request
+ * i (n_i new tokens, cached length L_i = lens[i]) and head h:
+ *   out = sum_t p_t v_t,  p = softmax over t of scale q . k_t,
+ * over t < L_i, and t <= L_i - n_i + j where causal is 1.  Decode steps (one new
+ * token), prompts and prompt chunks are causal = 1; a VAR scale step, whose tokens
+ * see each other, and attention to an encoder's states (lens = the states' lengths,
+ * cu of the queries) are causal = 0.  A row that sees nothing is 0.  Rows from
+ * cu[B] on are not written; slots is not read (may be NULL).
+ * Q: n_tokens rows of heads x head_dim, dtype; out: the same; strides in
+ * elements, multiples of 8.  fp32 scores, maxima, sums and accumulators; weights
+ * are rounded to fp16 for the second product.  Results do not depend on timing.
+ * A block number outside the pool is left out, a length above max_len or more
+ * than max_new new tokens cut; each is recorded for svdq_get_status
+ * (SVDQ_ERR_INVALID_ARG).  workspace: 16-byte aligned, >= the bytes below
+ * (which depend on the host numbers alone), not shared by calls that may overlap.
+ */
+size_t svdq_paged_attention_workspace_bytes(const svdq_paged_cache* c, const svdq_paged_batch* b);
+svdq_status svdq_paged_attention(const svdq_paged_cache* c, const svdq_paged_batch* b, const void* Q, int64_t q_stride,
+                                 int32_t causal, float scale, void* out, int64_t out_stride, void* workspace,
+                                 size_t ws_bytes, svdq_stream stream);
+
 /* Device workspace bytes svdq_linear needs for M tokens. */
 size_t svdq_workspace_bytes(const svdq_params* p, int64_t M);
 

@@ -24,12 +24,27 @@ INT4_G64, NVFP4 = 1, 2
 F16, BF16 = 1, 2
 FMT = {"int4": INT4_G64, "nvfp4": NVFP4}
 DTYPE = {"fp16": F16, "bf16": BF16}
+KV_FMT = {"int8": 1, "e4m3": 2}
 
 
 class svdq_params(ctypes.Structure):
     _fields_ = [("K", ctypes.c_int32), ("N", ctypes.c_int32), ("rank", ctypes.c_int32),
                 ("fmt", ctypes.c_int32), ("act_dtype", ctypes.c_int32), ("smooth", ctypes.c_int32),
                 ("alpha", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class svdq_paged_cache(ctypes.Structure):
+    _fields_ = [("kcodes", ctypes.c_void_p), ("kscale", ctypes.c_void_p), ("vcodes", ctypes.c_void_p),
+                ("vscale", ctypes.c_void_p), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32), ("n_blocks", ctypes.c_int32),
+                ("fmt", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class svdq_paged_batch(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("cu", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("B", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("n_tokens", ctypes.c_int32), ("max_new", ctypes.c_int32), ("max_len", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class SVDQError(RuntimeError):
@@ -60,6 +75,10 @@ def _load():
         "svdq_kv_attention_workspace_bytes": (sz, [i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
         "svdq_kv_attention": (ctypes.c_int, [vp, ctypes.c_int32, vp, vp, vp, vp, vp, vp, i64, ctypes.c_int32,
                                              ctypes.c_int32, ctypes.c_int32, vp, vp, sz, vp]),
+        "svdq_paged_plan": (ctypes.c_int, [vp, ctypes.c_int32, ctypes.c_int32, vp, vp, vp, vp, vp, vp]),
+        "svdq_paged_append": (ctypes.c_int, [vp, vp, vp, i64, vp, i64, vp]),
+        "svdq_paged_attention_workspace_bytes": (sz, [vp, vp]),
+        "svdq_paged_attention": (ctypes.c_int, [vp, vp, vp, i64, ctypes.c_int32, ctypes.c_float, vp, i64, vp, sz, vp]),
         "svdq_workspace_bytes": (sz, [P, i64]),
         "svdq_linear": (ctypes.c_int, [P, vp, vp, i64, vp, vp, sz, vp]),
         "svdq_quantize_act": (ctypes.c_int, [P, vp, vp, i64, vp, sz, vp]),
@@ -88,7 +107,8 @@ EXPORTED = ("svdq_blob_bytes", "svdq_prepare", "svdq_blob_check", "svdq_blob_exp
             "svdq_status_string", "svdq_last_error_string", "svdq_probe_cvt", "svdq_probe_div", "svdq_probe_tc",
             "svdq_linear_noalloc", "svdq_probe_timeout", "svdq_kv_workspace_bytes", "svdq_kv_encode",
             "svdq_kv_decode", "svdq_kv_attention_workspace_bytes", "svdq_kv_attention",
-            "svdq_chain_workspace_bytes", "svdq_gemm_chain")
+            "svdq_chain_workspace_bytes", "svdq_gemm_chain", "svdq_paged_plan", "svdq_paged_append",
+            "svdq_paged_attention_workspace_bytes", "svdq_paged_attention")
 NOALLOC_SCRATCH_BYTES = 16 << 20   # SVDQ_NOALLOC_SCRATCH_BYTES
 
 
@@ -266,6 +286,93 @@ def kv_attention(Q, Mq: int, kcodes, kscale, kzero, vcodes, vscale, vzero, T: in
                                 _ptr(vzero), T, C, heads, DTYPE[dtype], _ptr(out), _ptr(workspace),
                                 workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "svdq_kv_attention")
+
+
+def _expect(ok: bool, what: str):
+    if not ok:
+        raise SVDQError(ERR_INVALID_ARG, what)
+
+
+def _words(t, n: int, name: str) -> int:
+    """Address of a contiguous int32 tensor of at least n values."""
+    import torch
+    _expect(t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= n, f"{name}: contiguous int32, {n} values")
+    return t.data_ptr()
+
+
+def paged_cache(heads: int, kv_heads: int, head_dim: int, block_size: int, n_blocks: int, fmt: str, dtype: str,
+                kcodes, kscale, vcodes, vscale) -> svdq_paged_cache:
+    """The pool of a paged 8-bit KV cache over the caller's device buffers: codes n_blocks x kv_heads x
+    block_size x head_dim bytes, scales n_blocks x kv_heads fp32.  Keeps the tensors alive."""
+    c = svdq_paged_cache(None, None, None, None, heads, kv_heads, head_dim, block_size, n_blocks, KV_FMT[fmt],
+                         DTYPE[dtype], 0)
+    cells = n_blocks * kv_heads
+    for name, t, n in (("kcodes", kcodes, cells * block_size * head_dim), ("vcodes", vcodes, cells * block_size * head_dim),
+                       ("kscale", kscale, 4 * cells), ("vscale", vscale, 4 * cells)):
+        _expect(t.is_contiguous() and t.numel() * t.element_size() >= n, f"paged_cache: {name}, contiguous, {n} bytes")
+        setattr(c, name, t.data_ptr())
+    c.tensors, c.ref = (kcodes, kscale, vcodes, vscale), ctypes.addressof(c)
+    c.q_cols, c.kv_cols = heads * head_dim, kv_heads * head_dim
+    return c
+
+
+def paged_batch(table, lens, cu, slots=None, *, max_new: int, max_len: int,
+                n_tokens: int | None = None) -> svdq_paged_batch:
+    """One step's requests: table B x max_blocks, lens B, cu B + 1, slots n_tokens (device int32; slots may be
+    None for attention alone, with n_tokens given).  max_new and max_len bound the requests' new tokens and
+    cached lengths.  Keeps the tensors alive."""
+    B, max_blocks = table.shape
+    n = slots.numel() if n_tokens is None else n_tokens
+    _expect(n_tokens is None or slots is None or slots.numel() >= n, "paged_batch: slots")
+    b = svdq_paged_batch(_words(table, B * max_blocks, "table"), _words(lens, B, "lens"), _words(cu, B + 1, "cu"),
+                         None if slots is None else _words(slots, n, "slots"), B, max_blocks, n, max_new, max_len, 0)
+    b.tensors, b.ref = (table, lens, cu, slots), ctypes.addressof(b)
+    return b
+
+
+def paged_plan(batch: svdq_paged_batch, block_size: int, prev, target, ring, state_in, state_out, stream=None):
+    """Lengths prev -> target (device int32, B each): takes blocks from the free ring or gives them back and
+    writes the batch's table, lens, cu and slots; state_out = {head, count, lacking, new tokens}."""
+    _check(_lib.svdq_paged_plan(batch.ref, block_size, ring.numel(), _words(prev, batch.B, "prev"),
+                                _words(target, batch.B, "target"), _words(ring, 1, "ring"),
+                                _words(state_in, 4, "state_in"), _words(state_out, 4, "state_out"),
+                                _stream(stream)), "svdq_paged_plan")
+
+
+def _rows16(t, n: int, cols: int, dtype: int, name: str) -> tuple[int, int]:
+    """Address and row stride (elements) of n rows of `cols` values (any trailing shape, contiguous in a row)."""
+    import torch
+    ok = t.dtype == (torch.bfloat16 if dtype == BF16 else torch.float16) and t.shape[0] >= n
+    if t.dim() == 2:
+        ok = ok and t.shape[1] == cols and t.stride(1) == 1
+    else:
+        ok = ok and t.dim() == 3 and t.shape[1] * t.shape[2] == cols and t.stride(2) == 1 and \
+            (t.shape[1] == 1 or t.stride(1) == t.shape[2])
+    _expect(ok, f"{name}: {n} rows of {cols} values in the cache's dtype, contiguous within a row")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(cols, t.stride(0)))
+
+
+def paged_append(cache: svdq_paged_cache, batch: svdq_paged_batch, K, V, stream=None):
+    """Quantises the step's keys and values (n_tokens rows of kv_heads x head_dim, row strides free) into the cache."""
+    k, ks = _rows16(K, batch.n_tokens, cache.kv_cols, cache.dtype, "K")
+    v, vs = _rows16(V, batch.n_tokens, cache.kv_cols, cache.dtype, "V")
+    _check(_lib.svdq_paged_append(cache.ref, batch.ref, k, ks, v, vs, _stream(stream)), "svdq_paged_append")
+
+
+def paged_attention_workspace_bytes(cache: svdq_paged_cache, batch: svdq_paged_batch) -> int:
+    return _lib.svdq_paged_attention_workspace_bytes(cache.ref, batch.ref)
+
+
+def paged_attention(cache: svdq_paged_cache, batch: svdq_paged_batch, Q, out, workspace, causal: bool = True,
+                    scale: float | None = None, stream=None):
+    """Attention of the step's queries (n_tokens rows of heads x head_dim) over the cache into out (as Q);
+    scale None: 1 / sqrt(head_dim)."""
+    q, qs = _rows16(Q, batch.n_tokens, cache.q_cols, cache.dtype, "Q")
+    o, os_ = _rows16(out, batch.n_tokens, cache.q_cols, cache.dtype, "out")
+    _check(_lib.svdq_paged_attention(cache.ref, batch.ref, q, qs, int(bool(causal)),
+                                     cache.head_dim ** -0.5 if scale is None else scale, o, os_, workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), _stream(stream)),
+           "svdq_paged_attention")
 
 
 def linear_noalloc(p: svdq_params, blob_dev, X, M: int, Y, stream=None):

@@ -1,0 +1,1036 @@
+// Paged 8-bit KV cache: the step plan, the append and the attention that reads
+// the cache (the serving form of the INT8 KV cache of "VAR-Compressor：在边缘GPU上
+// 实现80亿参数视觉自回归模型的高效量化部署", INT8 KV缓存量化; the block-wise scale is
+// the granularity that lets tokens join a cache without touching other blocks).
+//
+// Block b of the pool holds, for every key/value head h, `bs` tokens of d 8-bit
+// codes (contiguous bs x d bytes at ((b kv + h) bs d)) and one fp32 scale for the
+// keys and one for the values (at b kv + h): x ~ code * scale.
+#include <cuda_fp16.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "../../include/svdq.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace svdq {
+namespace paged {
+
+using namespace svdq::dev;
+
+constexpr int kMaxRequests = 16384;
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+// ------------------------------------------------------------------ step plan
+// new_i = max(0, target_i - prev_i); request i needs ceil(target/bs) -
+// ceil(prev/bs) more blocks (taken from the front of the free ring in request
+// order) or gives that many back (appended at its end).  Every CTA scans all B
+// requests (three exclusive sums: new tokens, blocks taken, blocks given) into
+// its own shared memory and then writes its share of the outputs, so one launch
+// needs no communication between CTAs.  A token's block is found without reading
+// what another CTA writes: blocks below ceil(prev/bs) come from the table, later
+// ones from the ring.  Latency-bound: the lengths' load, the scan, one search.
+constexpr int kPlanThreads = 512;
+
+struct PlanArgs {
+  const int* prev;
+  const int* target;
+  int* table;
+  int* lens;
+  int* cu;
+  int* slots;
+  int* ring;
+  const int* state_in;
+  int* state_out;
+  int B, max_blocks, n_tokens, max_new, max_len, n_blocks, lb;
+};
+
+__device__ __forceinline__ int blocks_of(int tokens, int lb) {
+  return (int)(((int64_t)tokens + ((1 << lb) - 1)) >> lb);
+}
+
+// Largest i in [0, n) with pre[i] <= k, for a non-decreasing pre with pre[0] = 0.
+__device__ __forceinline__ int last_not_above(const int* pre, int n, int k) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= k) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs A) {
+  extern __shared__ int plan_smem[];
+  int* s_new = plan_smem;            // [B + 1] exclusive sums
+  int* s_take = s_new + A.B + 1;
+  int* s_give = s_take + A.B + 1;
+  __shared__ long long w_new[kPlanThreads / 32];
+  __shared__ int w_take[kPlanThreads / 32], w_give[kPlanThreads / 32], s_bad;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  const int head = A.state_in[0], count = A.state_in[1];
+  long long c_new = 0;
+  int c_take = 0, c_give = 0;
+  bool bad = head < 0 || head >= A.n_blocks || count < 0 || count > A.n_blocks;
+  for (int i0 = 0; i0 < A.B; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    long long vn = 0;
+    int vt = 0, vg = 0;
+    if (i < A.B) {
+      const int p = A.prev[i], t = A.target[i];
+      if (p < 0 || t < 0 || t > A.max_len || p > (A.max_blocks << A.lb) || t > (A.max_blocks << A.lb) ||
+          (t > p && t - p > A.max_new)) {
+        bad = true;
+      } else {
+        const int a = blocks_of(p, A.lb), b = blocks_of(t, A.lb);
+        vn = t > p ? t - p : 0;
+        vt = b > a ? b - a : 0;
+        vg = a > b ? a - b : 0;
+      }
+    }
+    long long n = vn;
+    int t = vt, g = vg;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long n1 = __shfl_up_sync(0xffffffffu, n, o);
+      const int t1 = __shfl_up_sync(0xffffffffu, t, o), g1 = __shfl_up_sync(0xffffffffu, g, o);
+      if (lane >= o) { n += n1; t += t1; g += g1; }
+    }
+    if (lane == 31) { w_new[warp] = n; w_take[warp] = t; w_give[warp] = g; }
+    __syncthreads();
+    long long bn = c_new;
+    int bt = c_take, bg = c_give;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < warp) { bn += w_new[w]; bt += w_take[w]; bg += w_give[w]; }
+      c_new += w_new[w]; c_take += w_take[w]; c_give += w_give[w];
+    }
+    if (i < A.B) {
+      s_new[i] = (int)(bn + n - vn);
+      s_take[i] = bt + t - vt;
+      s_give[i] = bg + g - vg;
+    }
+    __syncthreads();
+  }
+  if (bad) s_bad = 1;
+  if (tid == 0) { s_new[A.B] = (int)c_new; s_take[A.B] = c_take; s_give[A.B] = c_give; }
+  __syncthreads();
+  const bool wrong = s_bad != 0 || c_new > A.n_tokens || (int64_t)count - c_take + c_give > A.n_blocks;
+  const int lacking = wrong ? -1 : (c_take > count ? c_take - count : 0);
+  const bool ok = lacking == 0;
+  const int gtid = blockIdx.x * kPlanThreads + tid, stride = gridDim.x * kPlanThreads;
+  if (gtid == 0) {
+    // head may be out of range when the call is refused: handed through as it is
+    int h = head;
+    if (ok) { h = head + c_take; if (h >= A.n_blocks) h -= A.n_blocks; }
+    A.state_out[0] = h;
+    A.state_out[1] = ok ? count - c_take + c_give : count;
+    A.state_out[2] = lacking;
+    A.state_out[3] = ok ? (int)c_new : 0;
+  }
+  for (int i = gtid; i <= A.B; i += stride) {
+    A.cu[i] = ok ? s_new[i] : 0;
+    if (i < A.B) A.lens[i] = ok ? A.target[i] : A.prev[i];
+  }
+  const auto wrap = [&](int64_t k) { return (int)(k % A.n_blocks); };
+  if (ok) {
+    for (int k = gtid; k < c_take; k += stride) {
+      const int i = last_not_above(s_take, A.B, k);
+      A.table[(size_t)i * A.max_blocks + blocks_of(A.prev[i], A.lb) + (k - s_take[i])] = A.ring[wrap((int64_t)head + k)];
+    }
+    for (int k = gtid; k < c_give; k += stride) {
+      const int i = last_not_above(s_give, A.B, k);
+      A.ring[wrap((int64_t)head + count + k)] =
+          A.table[(size_t)i * A.max_blocks + blocks_of(A.target[i], A.lb) + (k - s_give[i])];
+    }
+  }
+  const int total = ok ? (int)c_new : 0;
+  for (int k = gtid; k < A.n_tokens; k += stride) {
+    int slot = -1;
+    if (k < total) {
+      const int i = last_not_above(s_new, A.B, k);
+      const int p = A.prev[i], pos = p + (k - s_new[i]), held = blocks_of(p, A.lb), c = pos >> A.lb;
+      const int blk = c < held ? A.table[(size_t)i * A.max_blocks + c] : A.ring[wrap((int64_t)head + s_take[i] + (c - held))];
+      slot = blk < 0 || blk >= A.n_blocks ? -1 : (blk << A.lb) + (pos & ((1 << A.lb) - 1));
+    }
+    A.slots[k] = slot;
+  }
+}
+
+// -------------------------------------------------------------------- append
+// One CTA per (block touched by a request's new tokens, kv head, keys or values).
+// s = max(s_old, max |x| / qmax), codes = round(x / s); codes of the tokens that
+// the block held before are re-rounded when s grows.  The new rows (at most one
+// block: bs d values) are read once and stay in registers between the maximum
+// and the codes.  Work index w -> request: request i owns the indices from
+// floor(cu_i / bs) + 2 i, which leaves it at least as many as it touches blocks
+// (<= floor(new / bs) + 2), so the grid needs only n_tokens and B on the host.
+constexpr int kAppendThreads = 128;
+
+template <int FMT> struct Fmt;
+template <> struct Fmt<SVDQ_KV_INT8> { static constexpr float qmax = 127.0f; };
+template <> struct Fmt<SVDQ_KV_E4M3> { static constexpr float qmax = 448.0f; };
+
+template <int DT>
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == SVDQ_BF16) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+// x / s as IEEE division rounds it: q = RN(x rs) is within an ulp, e = x - q s is
+// exact (one FMA), RN(q + e rs) is the correctly rounded quotient (Markstein) while
+// nothing under- or overflows; rs = 0 outside 2^-60 <= s <= 2^60 (division then).
+__device__ __forceinline__ float quotient(float x, float s, float rs) {
+  if (rs == 0.0f) return s > 0.0f ? __fdiv_rn(x, s) : 0.0f;
+  const float q = __fmul_rn(x, rs);
+  return __fmaf_rn(__fmaf_rn(-q, s, x), rs, q);
+}
+
+// Four values to four codes, round to nearest even, saturating.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  if constexpr (FMT == SVDQ_KV_INT8) {
+    const auto q = [](float x) { return (uint32_t)(clampi(__float2int_rn(x), -127, 127) & 0xFF); };
+    return q(a) | (q(b) << 8) | (q(c) << 16) | (q(d) << 24);
+  } else {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ float code_value(uint32_t byte) {
+  if constexpr (FMT == SVDQ_KV_INT8) {
+    return (float)(int8_t)byte;
+  } else {
+    // E4M3 -> fp16 of value / 256: the exponent field moves up by one place, exact for every finite code
+    const uint16_t h = (uint16_t)(((byte & 0x80u) << 8) | ((byte & 0x7Fu) << 7));
+    return __half2float(__ushort_as_half(h)) * 256.0f;
+  }
+}
+
+struct AppendArgs {
+  const uint16_t* x[2];    // keys, values
+  int64_t stride[2];       // elements between tokens
+  uint8_t* codes[2];
+  float* scale[2];
+  const int* cu;
+  const int* slots;
+  int B, n_tokens, kv, n_blocks;
+};
+
+template <int DT, int FMT, int D, int LB>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs A) {
+  constexpr int BS = 1 << LB, kPerRow = D / 8, kRows = kAppendThreads / kPerRow, kPass = BS / kRows > 0 ? BS / kRows : 1;
+  __shared__ float s_amax[kAppendThreads / 32];
+  const int tid = threadIdx.x, w = blockIdx.x, h = blockIdx.y, which = blockIdx.z;
+  // this work item's request: the last one whose first index is not above w
+  int i = -1;
+  for (int r0 = 0; r0 < A.B; r0 += kAppendThreads) {
+    const int r = r0 + tid;
+    const bool le = r < A.B && (clampi(A.cu[r], 0, A.n_tokens) >> LB) + 2 * r <= w;
+    i += __syncthreads_count(le);
+  }
+  if (i < 0) return;
+  const int a = clampi(A.cu[i], 0, A.n_tokens), e = clampi(A.cu[i + 1], 0, A.n_tokens);
+  if (a >= e) return;
+  const int j = w - (a >> LB) - 2 * i, o0 = A.slots[a] & (BS - 1);
+  const int64_t first = (int64_t)a + (j == 0 ? 0 : (int64_t)j * BS - o0);
+  if (first >= e) return;
+  const int t0 = (int)first;
+  const int slot0 = A.slots[t0];
+  if (slot0 < 0) return;                             // a padded token
+  const int blk = slot0 >> LB, off = slot0 & (BS - 1);
+  if (blk >= A.n_blocks) {
+    if (tid == 0) record_status(SVDQ_ERR_INVALID_ARG);
+    return;
+  }
+  const int rows = min(min(e, a + (j + 1) * BS - o0) - t0, BS - off);
+  const int c = tid % kPerRow, r0 = tid / kPerRow;
+  const uint16_t* x = A.x[which] + (int64_t)t0 * A.stride[which] + h * D + 8 * c;
+  const size_t cell = (size_t)blk * A.kv + h;
+  const float s_old = off > 0 ? A.scale[which][cell] : 0.0f;
+  uint4 v[kPass];
+  uint32_t have = 0;
+#pragma unroll
+  for (int p = 0; p < kPass; ++p) {
+    const int r = r0 + p * kRows;
+    v[p] = make_uint4(0, 0, 0, 0);
+    // a row counts only where the slot map puts it next to the block's first new row
+    if (r < rows && A.slots[t0 + r] == slot0 + r) {
+      v[p] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)r * A.stride[which]));
+      have |= 1u << p;
+    }
+  }
+  float amax = 0.0f;
+#pragma unroll
+  for (int p = 0; p < kPass; ++p) {
+    float f[8];
+    unpack8<DT>(v[p], f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if ((tid & 31) == 0) s_amax[tid >> 5] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kAppendThreads / 32; ++k) amax = fmaxf(amax, s_amax[k]);
+  const float s = fmaxf(s_old, __fdiv_rn(amax, Fmt<FMT>::qmax));
+  uint8_t* base = A.codes[which] + cell * (size_t)(BS * D);
+  if (s > s_old) {
+    if (tid == 0) A.scale[which][cell] = s;
+    const float ratio = __fdiv_rn(s_old, s);
+    for (int p = tid; p < off * D / 16; p += kAppendThreads) {
+      uint4* at = reinterpret_cast<uint4*>(base) + p;
+      uint4 q = *at;
+      uint32_t* u = &q.x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float f[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) f[b] = __fmul_rn(code_value<FMT>((u[k] >> (8 * b)) & 0xFFu), ratio);
+        u[k] = codes4<FMT>(f[0], f[1], f[2], f[3]);
+      }
+      *at = q;
+    }
+  } else if (off == 0 && tid == 0) {
+    A.scale[which][cell] = 0.0f;                     // a fresh block of zeros
+  }
+  const float rs = s >= 0x1p-60f && s <= 0x1p+60f ? __frcp_rn(s) : 0.0f;
+#pragma unroll
+  for (int p = 0; p < kPass; ++p) {
+    if (have >> p & 1u) {
+      float f[8];
+      unpack8<DT>(v[p], f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = quotient(f[k], s, rs);
+      *reinterpret_cast<uint2*>(base + (size_t)(off + r0 + p * kRows) * D + 8 * c) =
+          make_uint2(codes4<FMT>(f[0], f[1], f[2], f[3]), codes4<FMT>(f[4], f[5], f[6], f[7]));
+    }
+  }
+}
+
+// ----------------------------------------------------------------- attention
+// Row r of request i, kv head h: new token r / G, query head h G + r % G.  With
+// codes c and scales s per block: x_t = scale 2^e s_k (q' . c_t) log2(e), where
+// q' = q 2^-e in fp16 (e: exponent of the row's largest entry, so q' is exact up to
+// 2^-25 of that entry); out = sum_t p_t s_v c^v_t / sum_t p_t, p_t = 2^(x_t - m).
+// Both products run on fp16 operands (8-bit codes are exact in fp16) with fp32
+// accumulators.  The value scale is folded into p before it is rounded to fp16,
+// relative to the largest value scale seen so far (p' <= 1, no overflow; one
+// rounding of 2^-11 per weight, the size of the rounding of an fp16 output).
+struct AttnArgs {
+  const uint16_t* q;
+  uint16_t* out;
+  const uint8_t* kc;
+  const uint8_t* vc;
+  const float* ks;
+  const float* vs;
+  const int* table;
+  const int* lens;
+  const int* cu;
+  float* part_o;           // [splits][n_tokens][heads][d]
+  float* part_ml;          // [splits][n_tokens][heads][2]
+  int64_t q_stride, out_stride;
+  int B, max_blocks, n_tokens, max_new, max_len, n_blocks, heads, kv, G, lb, causal, splits, chunk;
+  float scale_log2;
+};
+
+// What one request's rows see.
+struct Rows {
+  int a, n, L, rows;       // first token, new tokens, cached length, n G
+};
+__device__ __forceinline__ Rows request_rows(const AttnArgs& A, int i) {
+  Rows R;
+  R.a = clampi(A.cu[i], 0, A.n_tokens);
+  const int e = clampi(A.cu[i + 1], 0, A.n_tokens), n = e - R.a, L = A.lens[i];
+  R.n = clampi(n, 0, A.max_new);
+  R.L = clampi(L, 0, min(A.max_len, A.max_blocks << A.lb));
+  if (threadIdx.x == 0 && (n > A.max_new || L > R.L)) record_status(SVDQ_ERR_INVALID_ARG);
+  R.rows = R.n * A.G;
+  return R;
+}
+// Tokens that row r sees (its new token is r / G).
+__device__ __forceinline__ int seen_by(const AttnArgs& A, const Rows& R, int r) {
+  return A.causal ? max(0, R.L - R.n + r / A.G + 1) : R.L;
+}
+
+template <int DT>
+__device__ __forceinline__ float load16(uint16_t h) {
+  if constexpr (DT == SVDQ_BF16) return __uint_as_float((uint32_t)h << 16);
+  else return __half2float(__ushort_as_half(h));
+}
+template <int DT>
+__device__ __forceinline__ uint16_t store16(float f) {
+  if constexpr (DT == SVDQ_BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(f));
+  else return __half_as_ushort(__float2half_rn(f));
+}
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two codes (in bytes 0 and 1, or 2 and 3, of w) to an fp16 pair: the value for
+// int8, value / 256 for E4M3 (kUnit undoes it).  int8: the byte with its sign bit
+// flipped is u = code + 128; 0x6400 | u is the fp16 number 1024 + u.
+template <int FMT> constexpr float kUnit = FMT == SVDQ_KV_INT8 ? 1.0f : 256.0f;
+template <int FMT>
+__device__ __forceinline__ uint32_t pre(uint32_t w) {
+  return FMT == SVDQ_KV_INT8 ? w ^ 0x80808080u : w;
+}
+template <int FMT, int HI>
+__device__ __forceinline__ uint32_t half2_of(uint32_t w) {
+  if constexpr (FMT == SVDQ_KV_INT8) {
+    const uint32_t x = __byte_perm(w, 0x64646464u, HI ? 0x4342 : 0x4140);
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const uint32_t x = __byte_perm(w, 0u, HI ? 0x3424 : 0x1404);
+    return (x & 0x80008000u) | ((x >> 1) & 0x3F803F80u);
+  }
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16 rows of queries as normalised fp16 in shared memory (row pitch D + 8) and
+// each row's factor 2^e scale log2(e).  Rows past the request's are zero.
+template <int DT, int D>
+__device__ __forceinline__ void load_queries(const AttnArgs& A, const Rows& R, int h, int r0, int nrows, __half* sq,
+                                             float* sf, int warp, int nwarps, int lane) {
+  for (int rr = warp; rr < nrows; rr += nwarps) {
+    const int r = r0 + rr;
+    float v[D / 32], top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) v[k] = 0.0f;
+    if (r < R.rows) {
+      const uint16_t* q = A.q + (int64_t)(R.a + r / A.G) * A.q_stride + (int64_t)(h * A.G + r % A.G) * D;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) { v[k] = load16<DT>(q[lane + 32 * k]); top = fmaxf(top, fabsf(v[k])); }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int e = clampi((int)(__float_as_uint(top) >> 23) - 127, -100, 100);
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) sq[rr * (D + 8) + lane + 32 * k] = __float2half_rn(v[k] * down);
+    if (lane == 0) sf[rr] = __uint_as_float((uint32_t)(127 + e) << 23) * A.scale_log2;
+  }
+}
+
+// Few rows: 16 rows of one (request, kv head) against a range of its tokens.  Each
+// of the 4 warps takes every fourth tile of 32 tokens through a ring of its own
+// (bulk copies, no barrier between warps) and keeps its own m, l and accumulator;
+// the warps' results are joined at the end.  The mma.sync fragments are read
+// straight from the codes: the contraction's order over d is free, so a lane's 16
+// bytes of a key row serve 4 k-steps, and 16 bytes of four value rows 16 output
+// column tiles (column of tile j, index n: d = 16 n + j for d = 128).
+constexpr int kDecWarps = 4, kDecTile = 32;
+constexpr int dec_stages(int D) { return D == 128 ? 3 : 5; }
+constexpr int dec_ring_bytes(int D) { return kDecWarps * dec_stages(D) * kDecTile * D * 2; }
+struct DecMeta { float sk[2], sv[2]; };
+constexpr int dec_smem(int D) {
+  return dec_ring_bytes(D) + 16 * (D + 8) * 2 + kDecWarps * 64 * (16 + 8) + 16 * 4 + kDecWarps * 16 * 8 + 256;
+}
+
+template <int DT, int FMT, int D>
+__global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnArgs A) {
+  constexpr int NST = dec_stages(D), kStage = kDecTile * D * 2, NV = D / 8, KC = D / 64, VW = D / 32;
+  extern __shared__ __align__(128) uint8_t dsm[];
+  uint8_t* ring = dsm;
+  __half* sq = reinterpret_cast<__half*>(dsm + dec_ring_bytes(D));
+  DecMeta* meta = reinterpret_cast<DecMeta*>(sq + 16 * (D + 8));           // [warp][64]
+  int2* ids = reinterpret_cast<int2*>(meta + kDecWarps * 64);              // [warp][64]
+  float* sf = reinterpret_cast<float*>(ids + kDecWarps * 64);              // [16]
+  float2* wml = reinterpret_cast<float2*>(sf + 16);                        // [warp][16]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(wml + kDecWarps * 16);      // [warp][NST]
+  __shared__ int s_abort;
+  __shared__ float s_vref[kDecWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
+  const int rts = gridDim.y / A.kv, h = blockIdx.y / rts, r0 = (blockIdx.y % rts) * 16, req = blockIdx.z;
+  const int split = blockIdx.x;
+  griddep_launch();
+  const Rows R = request_rows(A, req);
+  if (r0 >= R.rows) return;
+  const int last = min(R.rows, r0 + 16) - 1;
+  const int vis = seen_by(A, R, last), first_vis = seen_by(A, R, r0);
+  const int t_begin = split * A.chunk, t_end = min(vis, t_begin + A.chunk);   // chunk is a multiple of 32
+  if (split > 0 && t_begin >= vis) return;
+  if (tid == 0) {
+    s_abort = 0;
+    for (int s = 0; s < kDecWarps * NST; ++s) mbar_init(&bars[s], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int tiles = t_end > t_begin ? (t_end - t_begin + kDecTile - 1) / kDecTile : 0;
+  const int mine = tiles > warp ? (tiles - warp + kDecWarps - 1) / kDecWarps : 0;
+  const int nblk = blocks_of(t_end, A.lb);
+  uint8_t* wring = ring + warp * NST * kStage;
+  uint64_t* wbar = bars + warp * NST;
+  DecMeta* wmeta = meta + warp * 64;
+  int2* wids = ids + warp * 64;
+  const size_t blk_bytes = (size_t)(D << A.lb);
+
+  // block ids and scales of 32 tiles at a time, a lane each
+  const auto load_group = [&](int k0) {
+    const int k = k0 + lane;
+    int2 id = make_int2(-1, -1);
+    DecMeta m = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+    if (k < mine) {
+      const int t = t_begin + (warp + kDecWarps * k) * kDecTile, c0 = t >> A.lb, c1 = (t + 16) >> A.lb;
+      const int* row = A.table + (size_t)req * A.max_blocks;
+      id.x = row[c0];
+      id.y = c1 == c0 ? id.x : (c1 < nblk ? row[c1] : -2);
+      if (id.x < 0 || id.x >= A.n_blocks) { id.x = -1; record_status(SVDQ_ERR_INVALID_ARG); }
+      if (id.y != -2 && (id.y < 0 || id.y >= A.n_blocks)) { id.y = -1; record_status(SVDQ_ERR_INVALID_ARG); }
+      if (id.x >= 0) { const size_t c = (size_t)id.x * A.kv + h; m.sk[0] = A.ks[c]; m.sv[0] = A.vs[c]; }
+      if (id.y >= 0) { const size_t c = (size_t)id.y * A.kv + h; m.sk[1] = A.ks[c]; m.sv[1] = A.vs[c]; }
+    }
+    wids[k & 63] = id;
+    wmeta[k & 63] = m;
+    __syncwarp();
+  };
+  const auto issue = [&](int k) {
+    if ((k & 31) == 0) load_group(k);
+    if (lane == 0) {
+      const int t = t_begin + (warp + kDecWarps * k) * kDecTile, o = t & ((1 << A.lb) - 1);
+      const int2 id = wids[k & 63];
+      uint8_t* dst = wring + (k % NST) * kStage;
+      uint64_t* bar = &wbar[k % NST];
+      if (A.lb >= 5) {
+        mbar_arrive_expect_tx(bar, id.x >= 0 ? 2 * kDecTile * D : 0);
+        if (id.x >= 0) {
+          const size_t at = ((size_t)id.x * A.kv + h) * blk_bytes + (size_t)o * D;
+          bulk_load(dst, A.kc + at, kDecTile * D, bar);
+          bulk_load(dst + kDecTile * D, A.vc + at, kDecTile * D, bar);
+        }
+      } else {
+        mbar_arrive_expect_tx(bar, (id.x >= 0 ? kDecTile * D : 0) + (id.y >= 0 ? kDecTile * D : 0));
+        if (id.x >= 0) {
+          const size_t at = ((size_t)id.x * A.kv + h) * blk_bytes;
+          bulk_load(dst, A.kc + at, 16 * D, bar);
+          bulk_load(dst + kDecTile * D, A.vc + at, 16 * D, bar);
+        }
+        if (id.y >= 0) {
+          const size_t at = ((size_t)id.y * A.kv + h) * blk_bytes;
+          bulk_load(dst + 16 * D, A.kc + at, 16 * D, bar);
+          bulk_load(dst + kDecTile * D + 16 * D, A.vc + at, 16 * D, bar);
+        }
+      }
+    }
+  };
+  for (int k = 0; k < min(mine, NST); ++k) issue(k);
+
+  load_queries<DT, D>(A, R, h, r0, 16, sq, sf, warp, kDecWarps, lane);
+  __syncthreads();
+  uint32_t qf[D / 16][4];
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) {
+    const int col = (s >> 2) * 64 + q4 * 16 + 4 * (s & 3);
+    const uint2 lo = *reinterpret_cast<const uint2*>(sq + g * (D + 8) + col);
+    const uint2 hi = *reinterpret_cast<const uint2*>(sq + (g + 8) * (D + 8) + col);
+    qf[s][0] = lo.x; qf[s][1] = hi.x; qf[s][2] = lo.y; qf[s][3] = hi.y;
+  }
+  const float f0 = sf[g] * kUnit<FMT>, f1 = sf[g + 8] * kUnit<FMT>;
+  const int see0 = r0 + g < R.rows ? min(t_end, seen_by(A, R, r0 + g)) : t_end;
+  const int see1 = r0 + g + 8 < R.rows ? min(t_end, seen_by(A, R, r0 + g + 8)) : t_end;
+  const int clear = min(t_end, first_vis);              // tiles that end at or below this need no mask
+  float o[NV][4];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f, vref = 0.0f;
+
+  for (int k = 0; k < mine; ++k) {
+    const int st = k % NST, t = t_begin + (warp + kDecWarps * k) * kDecTile;
+    if (!mbar_wait(&wbar[st], (k / NST) & 1, &s_abort)) break;
+    const uint8_t* kt = wring + st * kStage;
+    const uint8_t* vt = kt + kDecTile * D;
+    const DecMeta md = wmeta[k & 63];
+    const int2 id = wids[k & 63];
+    float x[4][4];
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        const uint4 w = *reinterpret_cast<const uint4*>(kt + (nt * 8 + g) * D + c * 64 + q4 * 16);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t y = pre<FMT>(u[i]);
+          mma16816(x[nt], qf[c * 4 + i], half2_of<FMT, 0>(y), half2_of<FMT, 1>(y));
+        }
+      }
+    // scores in units of log2, masked
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      const float sk = md.sk[nt >> 1];
+      x[nt][0] *= f0 * sk; x[nt][1] *= f0 * sk; x[nt][2] *= f1 * sk; x[nt][3] *= f1 * sk;
+    }
+    if (t + kDecTile > clear || id.x < 0 || id.y < 0) {
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        const bool gone = (nt < 2 ? id.x : id.y) < 0;
+        const int tt = t + nt * 8 + 2 * q4;
+        if (gone || tt >= see0) x[nt][0] = -INFINITY;
+        if (gone || tt + 1 >= see0) x[nt][1] = -INFINITY;
+        if (gone || tt >= see1) x[nt][2] = -INFINITY;
+        if (gone || tt + 1 >= see1) x[nt][3] = -INFINITY;
+      }
+    }
+    float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      a0 = fmaxf(a0, fmaxf(x[nt][0], x[nt][1]));
+      a1 = fmaxf(a1, fmaxf(x[nt][2], x[nt][3]));
+    }
+    a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 1)); a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
+    a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1)); a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
+    const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1), vmax = fmaxf(vref, fmaxf(md.sv[0], md.sv[1]));
+    if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1 || vmax > vref)) {
+      const float b0 = n0 == -INFINITY ? 1.0f : ex2(m0 - n0), b1 = n1 == -INFINITY ? 1.0f : ex2(m1 - n1);
+      const float fv = vmax > 0.0f ? __fdiv_rn(vref, vmax) : 1.0f;
+      l0 *= b0; l1 *= b1;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) { o[j][0] *= b0 * fv; o[j][1] *= b0 * fv; o[j][2] *= b1 * fv; o[j][3] *= b1 * fv; }
+      m0 = n0; m1 = n1; vref = vmax;
+    }
+    const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
+    const float rv = vref > 0.0f ? __fdiv_rn(1.0f, vref) : 0.0f;
+    uint32_t pa[2][4];
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      const float wv = md.sv[nt >> 1] * rv;
+      const float p0 = ex2(x[nt][0] - z0), p1 = ex2(x[nt][1] - z0), p2 = ex2(x[nt][2] - z1), p3 = ex2(x[nt][3] - z1);
+      l0 += p0 + p1;
+      l1 += p2 + p3;
+      pa[nt >> 1][(nt & 1) * 2] = pack_half2(p0 * wv, p1 * wv);
+      pa[nt >> 1][(nt & 1) * 2 + 1] = pack_half2(p2 * wv, p3 * wv);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint32_t u[4][VW];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint8_t* row = vt + (s * 16 + 2 * q4 + (r & 1) + (r >> 1) * 8) * D + g * (D / 8);
+        if constexpr (D == 128) {
+          const uint4 w = *reinterpret_cast<const uint4*>(row);
+          u[r][0] = pre<FMT>(w.x); u[r][1] = pre<FMT>(w.y); u[r][2] = pre<FMT>(w.z); u[r][3] = pre<FMT>(w.w);
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(row);
+          u[r][0] = pre<FMT>(w.x); u[r][1] = pre<FMT>(w.y);
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        const uint32_t la = __byte_perm(u[0][w], u[1][w], 0x5140), ha = __byte_perm(u[0][w], u[1][w], 0x7362);
+        const uint32_t lb = __byte_perm(u[2][w], u[3][w], 0x5140), hb = __byte_perm(u[2][w], u[3][w], 0x7362);
+        mma16816(o[4 * w + 0], pa[s], half2_of<FMT, 0>(la), half2_of<FMT, 0>(lb));
+        mma16816(o[4 * w + 1], pa[s], half2_of<FMT, 1>(la), half2_of<FMT, 1>(lb));
+        mma16816(o[4 * w + 2], pa[s], half2_of<FMT, 0>(ha), half2_of<FMT, 0>(hb));
+        mma16816(o[4 * w + 3], pa[s], half2_of<FMT, 1>(ha), half2_of<FMT, 1>(hb));
+      }
+    }
+    __syncwarp();
+    if (k + NST < mine) issue(k + NST);
+  }
+  // join the four warps: weights 2^(m_w - M) and the value reference of each
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 1); l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 1); l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+  if (q4 == 0) { wml[warp * 16 + g] = make_float2(m0, l0); wml[warp * 16 + g + 8] = make_float2(m1, l1); }
+  if (lane == 0) s_vref[warp] = vref * kUnit<FMT>;
+  __syncthreads();                                       // every ring is free: the accumulators go there
+  float* acc = reinterpret_cast<float*>(ring);           // [warp][16][D]
+  const auto weight = [&](int w, int r, float M) { const float m = wml[w * 16 + r].x; return m == -INFINITY ? 0.0f : ex2(m - M); };
+  {
+    float M0 = -INFINITY, M1 = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) { M0 = fmaxf(M0, wml[w * 16 + g].x); M1 = fmaxf(M1, wml[w * 16 + g + 8].x); }
+    const float w0 = weight(warp, g, M0) * s_vref[warp], w1 = weight(warp, g + 8, M1) * s_vref[warp];
+    // tile j, columns n = 2 q4, 2 q4 + 1: d = (D / 8) n + j
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float* p0 = acc + (warp * 16 + g) * D + (D / 8) * 2 * q4 + j;
+      float* p1 = p0 + 8 * D;
+      p0[0] = o[j][0] * w0; p0[D / 8] = o[j][1] * w0;
+      p1[0] = o[j][2] * w1; p1[D / 8] = o[j][3] * w1;
+    }
+  }
+  __syncthreads();
+  const bool whole = vis <= A.chunk;                     // this split holds all that the rows see
+  for (int idx = tid; idx < 16 * D / 4; idx += kDecWarps * 32) {
+    const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
+    if (r0 + r >= R.rows) break;
+    float M = -INFINITY, L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, wml[w * 16 + r].x);
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) L += weight(w, r, M) * wml[w * 16 + r].y;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      const float4 y = *reinterpret_cast<const float4*>(acc + (w * 16 + r) * D + d);
+      v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+    }
+    const int token = R.a + (r0 + r) / A.G, head = h * A.G + (r0 + r) % A.G;
+    if (whole) {
+      const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
+      uint2 w;
+      w.x = (uint32_t)store16<DT>(v.x * inv) | ((uint32_t)store16<DT>(v.y * inv) << 16);
+      w.y = (uint32_t)store16<DT>(v.z * inv) | ((uint32_t)store16<DT>(v.w * inv) << 16);
+      *reinterpret_cast<uint2*>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + d) = w;
+    } else {
+      const size_t cell = ((size_t)split * A.n_tokens + token) * A.heads + head;
+      *reinterpret_cast<float4*>(A.part_o + cell * D + d) = v;
+      if (d == 0) *reinterpret_cast<float2*>(A.part_ml + cell * 2) = make_float2(M, L);
+    }
+  }
+}
+
+// Joins the splits of a row in their order: one warp per row, rows whose tokens
+// fitted one split were written already.
+constexpr int kJoinWarps = 4;
+template <int DT, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnArgs A, int tile_rows) {
+  const int lane = threadIdx.x & 31, r = blockIdx.x * kJoinWarps + (threadIdx.x >> 5), h = blockIdx.y, req = blockIdx.z;
+  griddep_wait();
+  const Rows R = request_rows(A, req);
+  if (r >= R.rows) return;
+  const int vis = seen_by(A, R, min(R.rows, (r / tile_rows + 1) * tile_rows) - 1);
+  if (vis <= A.chunk) return;
+  const int n = (vis + A.chunk - 1) / A.chunk;
+  const int token = R.a + r / A.G, head = h * A.G + r % A.G;
+  const size_t cell = (size_t)token * A.heads + head, step = (size_t)A.n_tokens * A.heads;
+  float M = -INFINITY;
+  for (int s = lane; s < n; s += 32) M = fmaxf(M, A.part_ml[(cell + s * step) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.0f, v[D / 32];
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) v[k] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const size_t c = cell + s * step;
+    const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + c * 2);
+    const float w = ml.x == -INFINITY ? 0.0f : ex2(ml.x - M);
+    L += w * ml.y;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) v[k] += w * A.part_o[c * D + lane + 32 * k];
+  }
+  const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k)
+    A.out[(int64_t)token * A.out_stride + (int64_t)head * D + lane + 32 * k] = store16<DT>(v[k] * inv);
+}
+
+// ------------------------------------------------------------- host launchers
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+int log2_block(int bs) {
+  switch (bs) {
+    case 16: return 4;
+    case 32: return 5;
+    case 64: return 6;
+    case 128: return 7;
+    default: return -1;
+  }
+}
+
+svdq_status check_cache(const svdq_paged_cache* c) {
+  if (!c || c->reserved != 0) return SVDQ_ERR_INVALID_ARG;
+  if (c->heads < 1 || c->kv_heads < 1 || c->heads % c->kv_heads != 0 || c->n_blocks < 1 || c->heads > 65535)
+    return SVDQ_ERR_INVALID_ARG;
+  if ((c->fmt != SVDQ_KV_INT8 && c->fmt != SVDQ_KV_E4M3) || (c->dtype != SVDQ_BF16 && c->dtype != SVDQ_F16))
+    return SVDQ_ERR_INVALID_ARG;
+  if ((c->head_dim != 64 && c->head_dim != 128) || log2_block(c->block_size) < 0) return SVDQ_ERR_UNSUPPORTED;
+  if ((int64_t)c->n_blocks * c->block_size > INT32_MAX) return SVDQ_ERR_UNSUPPORTED;
+  if (!c->kcodes || !c->vcodes || !c->kscale || !c->vscale) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(c->kcodes) || !aligned16(c->vcodes) || !aligned16(c->kscale) || !aligned16(c->vscale))
+    return SVDQ_ERR_ALIGNMENT;
+  return SVDQ_OK;
+}
+
+svdq_status check_batch(const svdq_paged_batch* b, int bs) {
+  if (!b || b->reserved != 0) return SVDQ_ERR_INVALID_ARG;
+  if (b->B < 1 || b->B > kMaxRequests || b->max_blocks < 1 || b->n_tokens < 0 || b->max_new < 1 || b->max_len < 0)
+    return SVDQ_ERR_INVALID_ARG;
+  if ((int64_t)b->B * b->max_blocks > INT32_MAX || (int64_t)b->max_blocks * bs > INT32_MAX) return SVDQ_ERR_UNSUPPORTED;
+  if ((int64_t)b->max_len > (int64_t)b->max_blocks * bs) return SVDQ_ERR_INVALID_ARG;
+  return SVDQ_OK;
+}
+
+constexpr int plan_smem_bytes(int B) { return 3 * (B + 1) * 4; }
+
+// Per device, once: the sm_100 check, the SM count and the kernels' shared-memory
+// attributes.
+struct Device { std::atomic<int> state; int sms; };   // state: 0 unknown, 1 ready, 2 not an sm_100
+Device g_devices[64];
+
+template <int DT, int FMT, int D>
+cudaError_t rows_attr() {
+  return cudaFuncSetAttribute(paged_rows_kernel<DT, FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dec_smem(D));
+}
+
+svdq_status device_ready(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return SVDQ_ERR_UNSUPPORTED;
+  if (dev < 0 || dev >= 64) return SVDQ_ERR_UNSUPPORTED;
+  Device& d = g_devices[dev];
+  int state = d.state.load(std::memory_order_acquire);
+  if (state == 0) {
+    int major = 0, minor = 0, n = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return SVDQ_ERR_UNSUPPORTED;
+    if (major == 10 && minor == 0) {
+      e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               plan_smem_bytes(kMaxRequests));
+      if (e == cudaSuccess) e = rows_attr<SVDQ_BF16, SVDQ_KV_INT8, 64>();
+      if (e == cudaSuccess) e = rows_attr<SVDQ_BF16, SVDQ_KV_INT8, 128>();
+      if (e == cudaSuccess) e = rows_attr<SVDQ_BF16, SVDQ_KV_E4M3, 64>();
+      if (e == cudaSuccess) e = rows_attr<SVDQ_BF16, SVDQ_KV_E4M3, 128>();
+      if (e == cudaSuccess) e = rows_attr<SVDQ_F16, SVDQ_KV_INT8, 64>();
+      if (e == cudaSuccess) e = rows_attr<SVDQ_F16, SVDQ_KV_INT8, 128>();
+      if (e == cudaSuccess) e = rows_attr<SVDQ_F16, SVDQ_KV_E4M3, 64>();
+      if (e == cudaSuccess) e = rows_attr<SVDQ_F16, SVDQ_KV_E4M3, 128>();
+      if (e != cudaSuccess) return cuda_failure(e, "paged cache kernel attributes");
+      state = 1;
+    } else {
+      state = 2;
+    }
+    d.sms = n;
+    d.state.store(state, std::memory_order_release);
+  }
+  *sms = d.sms;
+  return state == 1 ? SVDQ_OK : SVDQ_ERR_UNSUPPORTED;
+}
+
+svdq_status launched(const char* where) {
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? SVDQ_OK : cuda_failure(e, where);
+}
+
+// How a call's tokens are split: `splits` ranges of `chunk` tokens (a multiple
+// of the kernel's tile round) for every (request, kv head, row tile).
+struct Split { int splits, chunk, row_tiles; };
+Split split_of(const svdq_paged_cache* c, const svdq_paged_batch* b) {
+  Split s;
+  const int64_t rows = (int64_t)b->max_new * (c->heads / c->kv_heads);
+  s.row_tiles = (int)((rows + 15) / 16);
+  const int64_t ctas = (int64_t)b->B * c->kv_heads * s.row_tiles;
+  const int unit = kDecWarps * kDecTile;
+  const int64_t most = (b->max_len + unit - 1) / unit;          // at least one round of tiles each
+  int64_t want = (2 * 296 + ctas - 1) / ctas;
+  want = std::max<int64_t>(1, std::min(want, std::max<int64_t>(most, 1)));
+  const int64_t len = std::max(b->max_len, 1);
+  s.chunk = (int)(((len + want - 1) / want + unit - 1) / unit * unit);
+  s.splits = (int)((len + s.chunk - 1) / s.chunk);
+  return s;
+}
+
+size_t attention_ws(const svdq_paged_cache* c, const svdq_paged_batch* b) {
+  const Split s = split_of(c, b);
+  if (s.splits <= 1) return 16;
+  return (size_t)s.splits * b->n_tokens * c->heads * (size_t)(c->head_dim + 2) * sizeof(float);
+}
+
+template <int DT, int FMT, int D>
+svdq_status launch_attention(const AttnArgs& A, const Split& s, cudaStream_t stream) {
+  if ((int64_t)A.kv * s.row_tiles > 65535) return SVDQ_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)s.splits, (unsigned)(A.kv * s.row_tiles), (unsigned)A.B);
+  paged_rows_kernel<DT, FMT, D><<<grid, kDecWarps * 32, dec_smem(D), stream>>>(A);
+  svdq_status st = launched("paged_rows_kernel launch");
+  if (st != SVDQ_OK || s.splits <= 1) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((A.max_new * A.G + kJoinWarps - 1) / kJoinWarps), (unsigned)A.kv, (unsigned)A.B);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_join_kernel<DT, D>, A, 16);
+  if (e != cudaSuccess) return cuda_failure(e, "paged_join_kernel launch");
+  return launched("paged_join_kernel launch");
+}
+
+template <int DT, int FMT, int D>
+svdq_status launch_append(const AppendArgs& A, int lb, dim3 grid, cudaStream_t s) {
+  switch (lb) {
+    case 4: paged_append_kernel<DT, FMT, D, 4><<<grid, kAppendThreads, 0, s>>>(A); break;
+    case 5: paged_append_kernel<DT, FMT, D, 5><<<grid, kAppendThreads, 0, s>>>(A); break;
+    case 6: paged_append_kernel<DT, FMT, D, 6><<<grid, kAppendThreads, 0, s>>>(A); break;
+    default: paged_append_kernel<DT, FMT, D, 7><<<grid, kAppendThreads, 0, s>>>(A); break;
+  }
+  return launched("paged_append_kernel launch");
+}
+
+// The call's dtype, format and head size as template arguments.
+template <class F>
+svdq_status by_types(const svdq_paged_cache* c, F f) {
+  const bool bf = c->dtype == SVDQ_BF16, i8 = c->fmt == SVDQ_KV_INT8, wide = c->head_dim == 128;
+#define SVDQ_PAGED_CASE(BF_, I8_, W_, DT_, FMT_, D_) \
+  if (bf == BF_ && i8 == I8_ && wide == W_) return f.template operator()<DT_, FMT_, D_>();
+  SVDQ_PAGED_CASE(true, true, true, SVDQ_BF16, SVDQ_KV_INT8, 128)
+  SVDQ_PAGED_CASE(true, true, false, SVDQ_BF16, SVDQ_KV_INT8, 64)
+  SVDQ_PAGED_CASE(true, false, true, SVDQ_BF16, SVDQ_KV_E4M3, 128)
+  SVDQ_PAGED_CASE(true, false, false, SVDQ_BF16, SVDQ_KV_E4M3, 64)
+  SVDQ_PAGED_CASE(false, true, true, SVDQ_F16, SVDQ_KV_INT8, 128)
+  SVDQ_PAGED_CASE(false, true, false, SVDQ_F16, SVDQ_KV_INT8, 64)
+  SVDQ_PAGED_CASE(false, false, true, SVDQ_F16, SVDQ_KV_E4M3, 128)
+  SVDQ_PAGED_CASE(false, false, false, SVDQ_F16, SVDQ_KV_E4M3, 64)
+#undef SVDQ_PAGED_CASE
+  return SVDQ_ERR_INVALID_ARG;
+}
+
+struct AppendCall {
+  const AppendArgs& A;
+  int lb;
+  dim3 grid;
+  cudaStream_t s;
+  template <int DT, int FMT, int D> svdq_status operator()() const { return launch_append<DT, FMT, D>(A, lb, grid, s); }
+};
+struct AttnCall {
+  const AttnArgs& A;
+  const Split& sp;
+  cudaStream_t s;
+  template <int DT, int FMT, int D> svdq_status operator()() const { return launch_attention<DT, FMT, D>(A, sp, s); }
+};
+
+}  // namespace paged
+
+cudaError_t paged_status_take(unsigned int* v) {
+  cudaError_t e = cudaMemcpyFromSymbol(v, dev::g_status, sizeof(*v));
+  if (e == cudaSuccess && *v != 0) {
+    const unsigned int z = 0;
+    e = cudaMemcpyToSymbol(dev::g_status, &z, sizeof(z));
+  }
+  return e;
+}
+
+}  // namespace svdq
+
+using namespace svdq;
+using namespace svdq::paged;
+
+extern "C" {
+
+svdq_status svdq_paged_plan(const svdq_paged_batch* b, int32_t block_size, int32_t n_blocks, const int32_t* prev,
+                            const int32_t* target, int32_t* ring, const int32_t* state_in, int32_t* state_out,
+                            svdq_stream stream) {
+  const int lb = log2_block(block_size);
+  if (lb < 0) return SVDQ_ERR_UNSUPPORTED;
+  svdq_status st = check_batch(b, block_size);
+  if (st != SVDQ_OK) return st;
+  if (n_blocks < 1 || !prev || !target || !ring || !state_in || !state_out || !b->table || !b->lens || !b->cu ||
+      (b->n_tokens > 0 && !b->slots))
+    return SVDQ_ERR_INVALID_ARG;
+  if ((int64_t)n_blocks * block_size > INT32_MAX) return SVDQ_ERR_UNSUPPORTED;
+  if (state_in == state_out || prev == b->lens || target == b->lens) return SVDQ_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = device_ready(&sms)) != SVDQ_OK) return st;
+  PlanArgs A;
+  A.prev = prev; A.target = target; A.table = b->table; A.lens = b->lens; A.cu = b->cu; A.slots = b->slots;
+  A.ring = ring; A.state_in = state_in; A.state_out = state_out;
+  A.B = b->B; A.max_blocks = b->max_blocks; A.n_tokens = b->n_tokens; A.max_new = b->max_new; A.max_len = b->max_len;
+  A.n_blocks = n_blocks; A.lb = lb;
+  // a CTA per 2048 slots: up to there one CTA's scan and writes are cheaper than another CTA's scan
+  const int ctas = (int)std::min<int64_t>(sms, std::max<int64_t>(1, ((int64_t)b->n_tokens + b->B + 2047) / 2048));
+  paged_plan_kernel<<<ctas, kPlanThreads, plan_smem_bytes(b->B), reinterpret_cast<cudaStream_t>(stream)>>>(A);
+  return launched("paged_plan_kernel launch");
+}
+
+svdq_status svdq_paged_append(const svdq_paged_cache* c, const svdq_paged_batch* b, const void* K, int64_t k_stride,
+                              const void* V, int64_t v_stride, svdq_stream stream) {
+  svdq_status st = check_cache(c);
+  if (st != SVDQ_OK) return st;
+  if ((st = check_batch(b, c->block_size)) != SVDQ_OK) return st;
+  if (b->n_tokens == 0) return SVDQ_OK;
+  if (!K || !V || !b->cu || !b->slots) return SVDQ_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)c->kv_heads * c->head_dim;
+  if (k_stride < row || v_stride < row) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V) || k_stride % 8 != 0 || v_stride % 8 != 0) return SVDQ_ERR_ALIGNMENT;
+  int sms = 0;
+  if ((st = device_ready(&sms)) != SVDQ_OK) return st;
+  AppendArgs A;
+  A.x[0] = static_cast<const uint16_t*>(K); A.x[1] = static_cast<const uint16_t*>(V);
+  A.stride[0] = k_stride; A.stride[1] = v_stride;
+  A.codes[0] = c->kcodes; A.codes[1] = c->vcodes; A.scale[0] = c->kscale; A.scale[1] = c->vscale;
+  A.cu = b->cu; A.slots = b->slots; A.B = b->B; A.n_tokens = b->n_tokens; A.kv = c->kv_heads; A.n_blocks = c->n_blocks;
+  const int lb = log2_block(c->block_size);
+  const dim3 grid((unsigned)((b->n_tokens >> lb) + 2 * b->B), (unsigned)c->kv_heads, 2u);
+  return by_types(c, AppendCall{A, lb, grid, reinterpret_cast<cudaStream_t>(stream)});
+}
+
+size_t svdq_paged_attention_workspace_bytes(const svdq_paged_cache* c, const svdq_paged_batch* b) {
+  if (check_cache(c) != SVDQ_OK || check_batch(b, c->block_size) != SVDQ_OK) return 0;
+  return attention_ws(c, b);
+}
+
+svdq_status svdq_paged_attention(const svdq_paged_cache* c, const svdq_paged_batch* b, const void* Q, int64_t q_stride,
+                                 int32_t causal, float scale, void* out, int64_t out_stride, void* workspace,
+                                 size_t ws_bytes, svdq_stream stream) {
+  svdq_status st = check_cache(c);
+  if (st != SVDQ_OK) return st;
+  if ((st = check_batch(b, c->block_size)) != SVDQ_OK) return st;
+  if (b->n_tokens == 0) return SVDQ_OK;
+  if (!Q || !out || !workspace || !b->cu || !b->lens || !b->table || (causal != 0 && causal != 1) || !std::isfinite(scale))
+    return SVDQ_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)c->heads * c->head_dim;
+  if (q_stride < row || out_stride < row) return SVDQ_ERR_INVALID_ARG;
+  if (ws_bytes < attention_ws(c, b)) return SVDQ_ERR_WORKSPACE;
+  if (!aligned16(Q) || !aligned16(out) || !aligned16(workspace) || q_stride % 8 != 0 || out_stride % 8 != 0)
+    return SVDQ_ERR_ALIGNMENT;
+  int sms = 0;
+  if ((st = device_ready(&sms)) != SVDQ_OK) return st;
+  const Split sp = split_of(c, b);
+  AttnArgs A;
+  A.q = static_cast<const uint16_t*>(Q); A.out = static_cast<uint16_t*>(out);
+  A.kc = c->kcodes; A.vc = c->vcodes; A.ks = c->kscale; A.vs = c->vscale;
+  A.table = b->table; A.lens = b->lens; A.cu = b->cu;
+  A.part_o = static_cast<float*>(workspace);
+  A.part_ml = A.part_o + (size_t)sp.splits * b->n_tokens * c->heads * c->head_dim;
+  A.q_stride = q_stride; A.out_stride = out_stride;
+  A.B = b->B; A.max_blocks = b->max_blocks; A.n_tokens = b->n_tokens; A.max_new = b->max_new; A.max_len = b->max_len;
+  A.n_blocks = c->n_blocks; A.heads = c->heads; A.kv = c->kv_heads; A.G = c->heads / c->kv_heads;
+  A.lb = log2_block(c->block_size); A.causal = causal; A.splits = sp.splits; A.chunk = sp.chunk;
+  A.scale_log2 = scale * 1.4426950408889634f;
+  return by_types(c, AttnCall{A, sp, reinterpret_cast<cudaStream_t>(stream)});
+}
+
+}  // extern "C"

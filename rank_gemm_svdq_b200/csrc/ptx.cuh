@@ -9,8 +9,8 @@ namespace svdq {
 namespace dev {
 
 // Device-side failure record (first error wins), read by svdq_get_status.
-// (Defined here: this header has a single translation unit.)
-__device__ unsigned int g_status = 0;
+// (One word per translation unit that includes this header.)
+static __device__ unsigned int g_status = 0;
 
 constexpr unsigned int kStatusTimeout = 8u;    // == SVDQ_ERR_TIMEOUT
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // a bounded wait gives up after ~1 s

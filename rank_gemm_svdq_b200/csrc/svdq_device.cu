@@ -38,6 +38,7 @@
 #include <mutex>
 #include <vector>
 
+#include "internal.h"
 #include "layout.h"
 #include "ptx.cuh"
 
@@ -2527,6 +2528,10 @@ cudaError_t launch_act(const svdq_params* p, dev::ActArgs a, int64_t Mp, cudaStr
 
 }  // namespace
 
+namespace svdq {
+svdq_status cuda_failure(cudaError_t e, const char* where) { return cuda_fail(e, where); }
+}  // namespace svdq
+
 namespace {
 
 svdq_status common_checks(const svdq_params* p, const void* blob_dev, int64_t M, const void* workspace,
@@ -2872,9 +2877,11 @@ svdq_status svdq_get_status(svdq_stream stream) {
     const unsigned int z = 0;
     e = cudaMemcpyToSymbol(dev::g_status, &z, sizeof(z));
     if (e != cudaSuccess) return cuda_fail(e, "svdq_get_status clear");
-    return (svdq_status)v;
   }
-  return SVDQ_OK;
+  unsigned int w = 0;
+  e = paged_status_take(&w);
+  if (e != cudaSuccess) return cuda_fail(e, "svdq_get_status (paged cache)");
+  return (svdq_status)(v != 0 ? v : w);
 }
 
 const char* svdq_last_error_string(void) { return g_last_error; }
