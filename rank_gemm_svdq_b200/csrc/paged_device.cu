@@ -719,6 +719,410 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
   }
 }
 
+// Many rows: 128 or 256 rows of one (request, kv head) against a range of its
+// tokens, on the tensor cores.  Codes become fp16 operands in shared memory once
+// per 128 tokens and serve both 128-row tiles: S = Q K^T (both operands from shared
+// memory, 128 x 128 fp32 in TMEM), P in fp16 over S's own columns, O += P V (P from
+// TMEM; V as it lies, token rows of 64 d, an MN-major operand).  Roles:
+//   warps 0-3, 4-7   softmax of row tile 0 / 1, a row per thread: maximum, weights,
+//                    sum; rescales O only when a maximum grew by more than 2^8
+//                    (weights stay below 2^8 in fp16)
+//   warps 8-11       codes -> fp16 (the next tile's codes already in registers)
+//   warp 12          issues the MMAs: S0 S1 | P0V S0' | P1V S1' | ...
+// The value scale goes into a weight's exponent, p' = 2^(x - m + log2(s_v / s_ref))
+// with s_ref the largest value scale of the range, so it costs nothing per weight;
+// the row sum takes each 16 tokens' sum times s_ref / s_v.
+constexpr int kTileThreads = 512, kTileTok = 128, kTileMeta = 4;
+struct TileMeta { float sk, lsv, rsv; int gone; };        // 16 tokens: key scale, log2(s_v / s_ref), s_ref / s_v
+constexpr int kTileHalf = 128 * 128;                      // 128 rows of 64 fp16, 128-byte swizzle
+constexpr int tile_bytes(int D) { return D / 64 * kTileHalf; }
+constexpr int tiles_smem(int D) { return 6 * tile_bytes(D) + 256 * 4 + kTileMeta * 8 * 16 + 128 + 1024; }
+
+// MN-major operand with the 128-byte swizzle: rows of 64 values (128 bytes) along K,
+// 8-row groups 1024 bytes apart, the next 64 values of MN kTileHalf further.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(kTileHalf >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], fp16 operands, fp32 accumulate.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 16 code bytes to 16 fp16 at columns 16 c .. of row r of an operand tile.
+template <int FMT>
+__device__ __forceinline__ void store_codes(uint8_t* tile, int r, int half, int c, const uint4& w) {
+  const uint32_t u[4] = {pre<FMT>(w.x), pre<FMT>(w.y), pre<FMT>(w.z), pre<FMT>(w.w)};
+  uint8_t* row = tile + half * kTileHalf + r * 128;
+  *reinterpret_cast<uint4*>(row + (((2 * c) ^ (r & 7)) << 4)) =
+      make_uint4(half2_of<FMT, 0>(u[0]), half2_of<FMT, 1>(u[0]), half2_of<FMT, 0>(u[1]), half2_of<FMT, 1>(u[1]));
+  *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (r & 7)) << 4)) =
+      make_uint4(half2_of<FMT, 0>(u[2]), half2_of<FMT, 1>(u[2]), half2_of<FMT, 0>(u[3]), half2_of<FMT, 1>(u[3]));
+}
+
+template <int DT, int FMT, int D>
+__global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const AttnArgs A, int cta_rows) {
+  constexpr int H = D / 64, TB = tile_bytes(D);
+  extern __shared__ uint8_t tsm_raw[];
+  uint8_t* tsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tsm_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* sq = tsm;                                       // [2 row tiles]
+  uint8_t* sk = sq + 2 * TB;                               // [2 stages]
+  uint8_t* sv = sk + 2 * TB;                               // [2 stages]
+  float* sf = reinterpret_cast<float*>(sv + 2 * TB);       // [256]
+  TileMeta* meta = reinterpret_cast<TileMeta*>(sf + 256);  // [kTileMeta][8]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(meta + kTileMeta * 8);
+  uint64_t *k_full = bars, *k_empty = bars + 2, *v_full = bars + 4, *v_empty = bars + 6, *s_full = bars + 8,
+           *p_full = bars + 10, *o_full = bars + 12;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ float s_ref;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // splits fastest, then kv heads and requests, then row CTAs: the longest rows of a prompt first
+  const int split = blockIdx.x % A.splits, cell_id = (blockIdx.x / A.splits) % (A.B * A.kv);
+  const int h = cell_id % A.kv, req = cell_id / A.kv, rts = (A.max_new * A.G + cta_rows - 1) / cta_rows;
+  const int r0 = (rts - 1 - (int)(blockIdx.x / A.splits / (A.B * A.kv))) * cta_rows;
+  griddep_launch();
+  const Rows R = request_rows(A, req);
+  if (r0 >= R.rows) return;
+  const int last = min(R.rows, r0 + cta_rows) - 1;
+  const int vis = seen_by(A, R, last);
+  const int t_begin = split * A.chunk, t_end = min(vis, t_begin + A.chunk);
+  if (split > 0 && t_begin >= vis) return;
+  const int row_tiles = last - r0 >= 128 ? 2 : 1;
+  // token tiles of a row tile: what its last row sees
+  const auto tiles_of = [&](int rt) {
+    const int e = min(t_end, seen_by(A, R, min(R.rows, r0 + rt * 128 + 128) - 1));
+    return e > t_begin ? (e - t_begin + kTileTok - 1) / kTileTok : 0;
+  };
+  const int n0 = tiles_of(0), n1 = row_tiles == 2 ? tiles_of(1) : 0, tiles = max(n0, n1);
+  const int nblk = blocks_of(t_end, A.lb);
+  const int* row = A.table + (size_t)req * A.max_blocks;
+
+  if (tid == 0) {
+    s_abort = 0;
+    s_ref = 0.0f;
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&k_full[s], 4);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 4);
+      mbar_init(&v_empty[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 128);
+      mbar_init(&o_full[s], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  // the largest value scale of the range (scales are not negative: their bits order them)
+  {
+    float top = 0.0f;
+    for (int c = (t_begin >> A.lb) + tid; c < nblk; c += kTileThreads) {
+      const int id = row[c];
+      if (id >= 0 && id < A.n_blocks) top = fmaxf(top, A.vs[(size_t)id * A.kv + h]);
+      else record_status(SVDQ_ERR_INVALID_ARG);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) atomicMax(reinterpret_cast<int*>(&s_ref), __float_as_int(top));
+  }
+  // queries, normalised, as the A operand; 16 (8) lanes a row
+  if (warp < 8) {
+    constexpr int PER = D / 8, RPI = 32 / PER;             // lanes per row, rows per instruction
+    const int c = lane % PER;
+#pragma unroll 4
+    for (int k = 0; k < 32 / RPI; ++k) {
+      const int rr = warp * 32 + k * RPI + lane / PER, r = r0 + rr;
+      if (warp * 32 + k * RPI >= row_tiles * 128) break;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (r <= last)
+        w = __ldg(reinterpret_cast<const uint4*>(A.q + (int64_t)(R.a + r / A.G) * A.q_stride + (int64_t)(h * A.G + r % A.G) * D) + c);
+      float v[8], top = 0.0f;
+      unpack8<DT>(w, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+#pragma unroll
+      for (int o = PER / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = clampi((int)(__float_as_uint(top) >> 23) - 127, -100, 100);
+      // the factor is kept non-negative (maxima are taken before it): a negative scale turns the query instead
+      const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), A.scale_log2);
+      uint8_t* dst = sq + (rr >> 7) * TB + (c >> 3) * kTileHalf + (rr & 127) * 128 + (((c & 7) ^ (rr & 7)) << 4);
+      *reinterpret_cast<uint4*>(dst) = make_uint4(pack_half2(v[0] * down, v[1] * down), pack_half2(v[2] * down, v[3] * down),
+                                                  pack_half2(v[4] * down, v[5] * down), pack_half2(v[6] * down, v[7] * down));
+      if (c == 0) sf[rr] = __uint_as_float((uint32_t)(127 + e) << 23) * fabsf(A.scale_log2) * kUnit<FMT>;
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = s_tmem;
+  const float vref = s_ref;
+
+  if (warp < 8) {
+    regs_inc<184>();
+    const int rt = warp >> 2, n = rt == 0 ? n0 : n1;
+    const uint32_t ts = tm + rt * 128 + ((uint32_t)(warp & 3) << 21), to = tm + 256 + rt * D + ((uint32_t)(warp & 3) << 21);
+    const int r = r0 + rt * 128 + (tid & 127);
+    const bool live = r <= last;
+    if (rt < row_tiles) {
+      const float f = sf[rt * 128 + (tid & 127)];
+      const int see = live ? min(t_end, seen_by(A, R, r)) : t_end;
+      const int clear = min(t_end, seen_by(A, R, r0 + rt * 128));
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < n; ++j) {
+        const int t = t_begin + j * kTileTok;
+        if (!mbar_wait(&s_full[rt], j & 1, &s_abort)) break;
+        tc_fence_after();
+        uint32_t x[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld_32cols(ts + 32 * q, x[q]);
+        tmem_ld_wait();
+        const TileMeta* M = meta + (j & (kTileMeta - 1)) * 8;
+        float a[8];
+        int gone = 0;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) { a[g] = f * M[g].sk; gone |= M[g].gone; }
+        if (t + kTileTok > clear || gone) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const int lim = M[g].gone ? 0 : see - t - 16 * g;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              uint32_t& y = x[g >> 1][(g & 1) * 16 + i];
+              y = __float_as_uint(i < lim ? __uint_as_float(y) * a[g] : -INFINITY);
+            }
+            a[g] = 1.0f;
+          }
+        }
+        float top = m;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          float y[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(x[g >> 1][(g & 1) * 16 + i]);
+#pragma unroll
+          for (int w = 8; w > 0; w >>= 1)
+#pragma unroll
+            for (int i = 0; i < w; ++i) y[i] = fmaxf(y[i], y[i + w]);
+          top = fmaxf(top, y[0] * a[g]);
+        }
+        // a new reference maximum only where it grew by 2^8 (or is the first one)
+        const bool grow = top > m + 8.0f;                  // m = -inf: any finite top
+        if (__any_sync(0xffffffffu, grow)) {
+          const float b = grow ? (m == -INFINITY ? 0.0f : ex2(m - top)) : 1.0f;
+          if (grow) m = top;
+          l *= b;
+          if (j > 0) {
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld_16cols(to + 16 * q, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * b);
+              tmem_st_16cols(to + 16 * q, o);
+            }
+          }
+        }
+        const float z = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int g2 = 0; g2 < 4; ++g2) {
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int g = 2 * g2 + k;
+            const float b = M[g].lsv - z;
+            float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float p0 = ex2(fmaf(__uint_as_float(x[g2][k * 16 + i]), a[g], b));
+              const float p1 = ex2(fmaf(__uint_as_float(x[g2][k * 16 + i + 1]), a[g], b));
+              s0 += p0;
+              s1 += p1;
+              p[k * 8 + i / 2] = pack_half2(p0, p1);
+            }
+            l = fmaf(s0 + s1, M[g].rsv, l);
+          }
+          tmem_st_16cols(ts + 16 * g2, p);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[rt]);
+      }
+      const bool whole = vis <= A.chunk;
+      const int token = R.a + r / A.G, head = h * A.G + r % A.G;
+      const bool ok = n == 0 || mbar_wait(&o_full[rt], 0, &s_abort);
+      tc_fence_after();
+      const size_t cell = ((size_t)split * A.n_tokens + token) * A.heads + head;
+      const float u = vref * kUnit<FMT>, mul = whole ? (l > 0.0f ? __fdiv_rn(u, l) : 0.0f) : u;
+      if (!whole && live) *reinterpret_cast<float2*>(A.part_ml + cell * 2) = make_float2(m, l);
+#pragma unroll
+      for (int q = 0; q < D / 16; ++q) {
+        uint32_t o[16];
+        if (n > 0 && ok) {
+          tmem_ld_16cols(to + 16 * q, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = 0;
+        }
+        if (live) {
+          float y[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(o[i]) * mul;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + 16 * q);
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = (uint32_t)store16<DT>(y[2 * i]) | ((uint32_t)store16<DT>(y[2 * i + 1]) << 16);
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          } else {
+            float4* dst = reinterpret_cast<float4*>(A.part_o + cell * D + 16 * q);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          }
+        }
+      }
+    }
+  } else if (warp < 12) {
+    regs_dec<96>();
+    const int w = warp - 8, c = lane & 3, rl = 32 * w + (lane >> 2);   // rows rl + 8 i
+    const size_t head_off = (size_t)h * (D << A.lb), blk_bytes = (size_t)A.kv * (D << A.lb);
+    uint4 kr[4 * H], vr[4 * H];
+    float g_sk = 0.0f, g_sv = 0.0f;
+    int g_gone = 0, id[4];
+    const auto ids = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = (t_begin + j * kTileTok + rl + 8 * i) >> A.lb;
+        const int v = b < nblk ? row[b] : -1;
+        id[i] = v < A.n_blocks ? v : -1;
+      }
+    };
+    const auto load = [&](const uint8_t* codes, int j, uint4 (&x)[4 * H]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int o = (t_begin + j * kTileTok + rl + 8 * i) & ((1 << A.lb) - 1);
+        const uint4* at = reinterpret_cast<const uint4*>(codes + (id[i] < 0 ? 0 : id[i]) * blk_bytes + head_off + (size_t)o * D) + c;
+#pragma unroll
+        for (int q = 0; q < H; ++q) x[i * H + q] = id[i] >= 0 ? __ldg(at + 4 * q) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    // scales of this warp's two groups of 16 tokens: lanes 0-15 and 16-31 hold the first's and the second's
+    const auto scales = [&]() {
+      const int b = lane < 16 ? id[0] : id[2];
+      g_gone = b < 0;
+      g_sk = b < 0 ? 0.0f : A.ks[(size_t)b * A.kv + h];
+      g_sv = b < 0 ? 0.0f : A.vs[(size_t)b * A.kv + h];
+    };
+    if (tiles > 0) {
+      ids(0);
+      load(A.kc, 0, kr);
+      load(A.vc, 0, vr);
+      scales();
+    }
+    for (int j = 0; j < tiles; ++j) {
+      const int st = j & 1;
+      if (j >= 2 && !mbar_wait(&k_empty[st], ((j >> 1) & 1) ^ 1, &s_abort)) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < H; ++q) store_codes<FMT>(sk + st * TB, rl + 8 * i, q, c, kr[i * H + q]);
+      if ((lane & 15) == 0) {
+        TileMeta* M = meta + (j & (kTileMeta - 1)) * 8 + 2 * w + (lane >> 4);
+        // a scale below 2^-60 of the largest counts as that: its values are lost beside it either way
+        const float ratio = vref > 0.0f ? fmaxf(__fdiv_rn(g_sv, vref), 0x1p-60f) : 1.0f;
+        *M = TileMeta{g_sk, log2f(ratio), __fdiv_rn(1.0f, ratio), g_gone};
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full[st]);
+      if (j + 1 < tiles) {
+        ids(j + 1);
+        load(A.kc, j + 1, kr);
+        scales();
+      }
+      if (j >= 2 && !mbar_wait(&v_empty[st], ((j >> 1) & 1) ^ 1, &s_abort)) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < H; ++q) store_codes<FMT>(sv + st * TB, rl + 8 * i, q, c, vr[i * H + q]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&v_full[st]);
+      if (j + 1 < tiles) load(A.vc, j + 1, vr);
+    }
+  } else {
+    regs_dec<48>();
+    if (warp == 12 && lane == 0) {
+      constexpr uint32_t kIdS = idesc_f16_f16(128, 128), kIdO = idesc_f16_f16(128, D) | (1u << 16);
+      const auto issue_s = [&](int rt, int j) {
+        const uint32_t a = smem_u32(sq + rt * TB), b = smem_u32(sk + (j & 1) * TB);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t o = (k >> 2) * kTileHalf + (k & 3) * 32;
+          mma_f16(tm + rt * 128, desc_k_sw128(a + o), desc_k_sw128(b + o), kIdS, k > 0);
+        }
+        mma_commit(&s_full[rt]);
+      };
+      const auto issue_o = [&](int rt, int j) {
+        const uint32_t b = smem_u32(sv + (j & 1) * TB);
+#pragma unroll
+        for (int k = 0; k < kTileTok / 16; ++k)
+          mma_f16_ts(tm + 256 + rt * D, tm + rt * 128 + 8 * k, desc_mn_sw128(b + k * 2048), kIdO, j > 0 || k > 0);
+      };
+      bool ok = tiles == 0 || mbar_wait(&k_full[0], 0, &s_abort);
+      if (ok && tiles > 0) {
+        tc_fence_after();
+        if (n0 > 0) issue_s(0, 0);
+        if (n1 > 0) issue_s(1, 0);
+        mma_commit(&k_empty[0]);
+      }
+      for (int j = 0; ok && j < tiles; ++j) {
+        ok = mbar_wait(&v_full[j & 1], (j >> 1) & 1, &s_abort);
+        if (ok && j + 1 < tiles) ok = mbar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, &s_abort);
+        for (int rt = 0; ok && rt < 2; ++rt) {
+          const int n = rt == 0 ? n0 : n1;
+          if (j >= n) continue;
+          ok = mbar_wait(&p_full[rt], j & 1, &s_abort);
+          if (!ok) break;
+          tc_fence_after();
+          issue_o(rt, j);
+          if (j + 1 < n) issue_s(rt, j + 1);
+          else mma_commit(&o_full[rt]);
+        }
+        if (!ok) break;
+        mma_commit(&v_empty[j & 1]);
+        if (j + 1 < tiles) mma_commit(&k_empty[(j + 1) & 1]);
+      }
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tm, 512);
+  }
+}
+
 // Joins the splits of a row in their order: one warp per row, rows whose tokens
 // fitted one split were written already.
 constexpr int kJoinWarps = 4;
@@ -800,7 +1204,10 @@ Device g_devices[64];
 
 template <int DT, int FMT, int D>
 cudaError_t rows_attr() {
-  return cudaFuncSetAttribute(paged_rows_kernel<DT, FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dec_smem(D));
+  const cudaError_t e =
+      cudaFuncSetAttribute(paged_rows_kernel<DT, FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dec_smem(D));
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(paged_tiles_kernel<DT, FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, tiles_smem(D));
 }
 
 svdq_status device_ready(int* sms) {
@@ -844,36 +1251,53 @@ svdq_status launched(const char* where) {
   return e == cudaSuccess ? SVDQ_OK : cuda_failure(e, where);
 }
 
-// How a call's tokens are split: `splits` ranges of `chunk` tokens (a multiple
-// of the kernel's tile round) for every (request, kv head, row tile).
-struct Split { int splits, chunk, row_tiles; };
-Split split_of(const svdq_paged_cache* c, const svdq_paged_batch* b) {
+// The SM count that the split aims at: fixed, so that workspace sizes can be asked
+// for without a device.
+constexpr int kSplitSms = 148;
+
+// How a call's rows and tokens are split: CTAs of `cta_rows` rows (16: the few-row
+// kernel, 128 or 256: the tensor-core kernel) x `splits` ranges of `chunk` tokens (a
+// multiple of 128).
+struct Split { int cta_rows, row_ctas, splits, chunk; };
+Split split_of(const svdq_paged_cache* c, const svdq_paged_batch* b, int sms) {
   Split s;
-  const int64_t rows = (int64_t)b->max_new * (c->heads / c->kv_heads);
-  s.row_tiles = (int)((rows + 15) / 16);
-  const int64_t ctas = (int64_t)b->B * c->kv_heads * s.row_tiles;
-  const int unit = kDecWarps * kDecTile;
-  const int64_t most = (b->max_len + unit - 1) / unit;          // at least one round of tiles each
-  int64_t want = (2 * 296 + ctas - 1) / ctas;
-  want = std::max<int64_t>(1, std::min(want, std::max<int64_t>(most, 1)));
-  const int64_t len = std::max(b->max_len, 1);
-  s.chunk = (int)(((len + want - 1) / want + unit - 1) / unit * unit);
+  const int64_t rows = (int64_t)b->max_new * (c->heads / c->kv_heads), cells = (int64_t)b->B * c->kv_heads;
+  const auto ctas = [&](int per) { return (rows + per - 1) / per * cells; };
+  int64_t target;                                   // CTAs wanted
+  int64_t least;                                    // tokens a split is worth
+  if (rows <= 16) {
+    s.cta_rows = 16; target = 4 * sms; least = kDecWarps * kDecTile;
+  } else {
+    s.cta_rows = ctas(256) >= sms || rows <= 128 ? (rows <= 128 ? 128 : 256) : 128;
+    target = sms; least = 1024;
+  }
+  s.row_ctas = (int)((rows + s.cta_rows - 1) / s.cta_rows);
+  const int64_t len = std::max(b->max_len, 1), n = ctas(s.cta_rows);
+  const int64_t want = std::max<int64_t>(1, std::min((target + n - 1) / n, (len + least - 1) / least));
+  s.chunk = (int)(((len + want - 1) / want + 127) / 128 * 128);
   s.splits = (int)((len + s.chunk - 1) / s.chunk);
   return s;
 }
 
 size_t attention_ws(const svdq_paged_cache* c, const svdq_paged_batch* b) {
-  const Split s = split_of(c, b);
+  const Split s = split_of(c, b, kSplitSms);
   if (s.splits <= 1) return 16;
   return (size_t)s.splits * b->n_tokens * c->heads * (size_t)(c->head_dim + 2) * sizeof(float);
 }
 
 template <int DT, int FMT, int D>
 svdq_status launch_attention(const AttnArgs& A, const Split& s, cudaStream_t stream) {
-  if ((int64_t)A.kv * s.row_tiles > 65535) return SVDQ_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)s.splits, (unsigned)(A.kv * s.row_tiles), (unsigned)A.B);
-  paged_rows_kernel<DT, FMT, D><<<grid, kDecWarps * 32, dec_smem(D), stream>>>(A);
-  svdq_status st = launched("paged_rows_kernel launch");
+  svdq_status st;
+  if (s.cta_rows == 16) {
+    const dim3 grid((unsigned)s.splits, (unsigned)(A.kv * s.row_ctas), (unsigned)A.B);
+    paged_rows_kernel<DT, FMT, D><<<grid, kDecWarps * 32, dec_smem(D), stream>>>(A);
+    st = launched("paged_rows_kernel launch");
+  } else {
+    const int64_t grid = (int64_t)s.splits * s.row_ctas * A.B * A.kv;
+    if (grid > INT32_MAX) return SVDQ_ERR_UNSUPPORTED;
+    paged_tiles_kernel<DT, FMT, D><<<(unsigned)grid, kTileThreads, tiles_smem(D), stream>>>(A, s.cta_rows);
+    st = launched("paged_tiles_kernel launch");
+  }
   if (st != SVDQ_OK || s.splits <= 1) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((A.max_new * A.G + kJoinWarps - 1) / kJoinWarps), (unsigned)A.kv, (unsigned)A.B);
@@ -884,7 +1308,7 @@ svdq_status launch_attention(const AttnArgs& A, const Split& s, cudaStream_t str
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_join_kernel<DT, D>, A, 16);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_join_kernel<DT, D>, A, s.cta_rows);
   if (e != cudaSuccess) return cuda_failure(e, "paged_join_kernel launch");
   return launched("paged_join_kernel launch");
 }
@@ -1018,7 +1442,7 @@ svdq_status svdq_paged_attention(const svdq_paged_cache* c, const svdq_paged_bat
     return SVDQ_ERR_ALIGNMENT;
   int sms = 0;
   if ((st = device_ready(&sms)) != SVDQ_OK) return st;
-  const Split sp = split_of(c, b);
+  const Split sp = split_of(c, b, kSplitSms);
   AttnArgs A;
   A.q = static_cast<const uint16_t*>(Q); A.out = static_cast<uint16_t*>(out);
   A.kc = c->kcodes; A.vc = c->vcodes; A.ks = c->kscale; A.vs = c->vscale;
