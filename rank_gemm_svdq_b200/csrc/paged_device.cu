@@ -271,16 +271,24 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
   const size_t cell = (size_t)blk * A.kv + h;
   const float s_old = off > 0 ? A.scale[which][cell] : 0.0f;
   uint4 v[kPass];
+  int at[kPass];
   uint32_t have = 0;
+  // rows and their slots at once; a row counts only where the slot map puts it next to
+  // the block's first new row
 #pragma unroll
   for (int p = 0; p < kPass; ++p) {
     const int r = r0 + p * kRows;
     v[p] = make_uint4(0, 0, 0, 0);
-    // a row counts only where the slot map puts it next to the block's first new row
-    if (r < rows && A.slots[t0 + r] == slot0 + r) {
+    at[p] = -1;
+    if (r < rows) {
       v[p] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)r * A.stride[which]));
-      have |= 1u << p;
+      at[p] = A.slots[t0 + r];
     }
+  }
+#pragma unroll
+  for (int p = 0; p < kPass; ++p) {
+    if (at[p] == slot0 + r0 + p * kRows) have |= 1u << p;
+    else v[p] = make_uint4(0, 0, 0, 0);
   }
   float amax = 0.0f;
 #pragma unroll
@@ -449,83 +457,108 @@ __device__ __forceinline__ void load_queries(const AttnArgs& A, const Rows& R, i
   }
 }
 
-// Few rows: 16 rows of one (request, kv head) against a range of its tokens.  Each
-// of the 4 warps takes every fourth tile of 32 tokens through a ring of its own
-// (bulk copies, no barrier between warps) and keeps its own m, l and accumulator;
-// the warps' results are joined at the end.  The mma.sync fragments are read
-// straight from the codes: the contraction's order over d is free, so a lane's 16
-// bytes of a key row serve 4 k-steps, and 16 bytes of four value rows 16 output
-// column tiles (column of tile j, index n: d = 16 n + j for d = 128).
-constexpr int kDecWarps = 4, kDecTile = 32;
-constexpr int dec_stages(int D) { return D == 128 ? 3 : 5; }
-constexpr int dec_ring_bytes(int D) { return kDecWarps * dec_stages(D) * kDecTile * D * 2; }
+// Few rows: up to 8 NB rows of one (request, kv head) against a range of its tokens.
+// Bound by the cache's bytes, so the products run on mma.sync with the codes as the
+// 16-row operand and the few rows as its 8 columns: S^T = K Q^T, O^T = V^T P^T (half
+// the MMAs and accumulators of the other way round).  Each of the 4 warps takes every
+// fourth tile of 32 tokens through a ring of its own (bulk copies, no barrier between
+// warps) and keeps its own m, l and accumulator; the warps' results are joined at the
+// end, then those of the CTAs of a cluster, which share the tokens of a (request, kv
+// head) evenly.  The fragments are read straight from the codes: the order of the
+// contraction over d is free, so 16 bytes of a key row serve 4 k-steps, and 16 bytes
+// of four value rows the 16 values of d that a lane needs.
+constexpr int kDecWarps = 4, kDecTile = 32, kDecStages = 2, kDecGroup = 16, kMaxCluster = 8;
+constexpr int dec_stage_bytes(int D) { return kDecTile * D * 2; }
+constexpr int dec_ring_bytes(int D) { return kDecWarps * kDecStages * dec_stage_bytes(D); }
 struct DecMeta { float sk[2], sv[2]; };
-constexpr int dec_smem(int D) {
-  return dec_ring_bytes(D) + 16 * (D + 8) * 2 + kDecWarps * 64 * (16 + 8) + 16 * 4 + kDecWarps * 16 * 8 + 256;
+constexpr int dec_smem(int D, int NB) {
+  return dec_ring_bytes(D) + 8 * NB * (D + 8) * 2 + kDecWarps * 2 * kDecGroup * (16 + 8) + kDecWarps * NB * 8 * 8 + 8 * NB * 4 +
+         kDecWarps * kDecStages * 8;
 }
 
-template <int DT, int FMT, int D>
-__global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnArgs A) {
-  constexpr int NST = dec_stages(D), kStage = kDecTile * D * 2, NV = D / 8, KC = D / 64, VW = D / 32;
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int DT>
+__device__ __forceinline__ void store_row4(uint16_t* dst, const float4& v, float mul) {
+  uint2 w;
+  w.x = (uint32_t)store16<DT>(v.x * mul) | ((uint32_t)store16<DT>(v.y * mul) << 16);
+  w.y = (uint32_t)store16<DT>(v.z * mul) | ((uint32_t)store16<DT>(v.w * mul) << 16);
+  *reinterpret_cast<uint2*>(dst) = w;
+}
+
+template <int DT, int FMT, int D, int NB>
+__global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnArgs A, int cluster) {
+  constexpr int NST = kDecStages, kStage = dec_stage_bytes(D), KC = D / 64, VW = D / 32, NR = 8 * NB;
   extern __shared__ __align__(128) uint8_t dsm[];
   uint8_t* ring = dsm;
   __half* sq = reinterpret_cast<__half*>(dsm + dec_ring_bytes(D));
-  DecMeta* meta = reinterpret_cast<DecMeta*>(sq + 16 * (D + 8));           // [warp][64]
-  int2* ids = reinterpret_cast<int2*>(meta + kDecWarps * 64);              // [warp][64]
-  float* sf = reinterpret_cast<float*>(ids + kDecWarps * 64);              // [16]
-  float2* wml = reinterpret_cast<float2*>(sf + 16);                        // [warp][16]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(wml + kDecWarps * 16);      // [warp][NST]
+  DecMeta* meta = reinterpret_cast<DecMeta*>(sq + NR * (D + 8));           // [warp][2 groups]
+  int2* ids = reinterpret_cast<int2*>(meta + kDecWarps * 2 * kDecGroup);   // [warp][2 groups]
+  float2* wml = reinterpret_cast<float2*>(ids + kDecWarps * 2 * kDecGroup);  // [warp][NR]
+  float* sf = reinterpret_cast<float*>(wml + kDecWarps * NR);              // [NR]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sf + NR);                   // [warp][NST]
   __shared__ int s_abort;
   __shared__ float s_vref[kDecWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
-  const int rts = gridDim.y / A.kv, h = blockIdx.y / rts, r0 = (blockIdx.y % rts) * 16, req = blockIdx.z;
-  const int split = blockIdx.x;
-  griddep_launch();
+  const int h = blockIdx.y, req = blockIdx.z, split = blockIdx.x;
+  if (!cluster) griddep_launch();
   const Rows R = request_rows(A, req);
-  if (r0 >= R.rows) return;
-  const int last = min(R.rows, r0 + 16) - 1;
-  const int vis = seen_by(A, R, last), first_vis = seen_by(A, R, r0);
-  const int t_begin = split * A.chunk, t_end = min(vis, t_begin + A.chunk);   // chunk is a multiple of 32
-  if (split > 0 && t_begin >= vis) return;
+  if (R.rows == 0) return;
+  const int vis = seen_by(A, R, R.rows - 1), first_vis = seen_by(A, R, 0);
+  // a cluster shares what the rows see; otherwise a fixed chunk a split
+  const int chunk = cluster ? ((vis + A.splits - 1) / A.splits + kDecTile - 1) / kDecTile * kDecTile : A.chunk;
+  const int t_begin = split * chunk, t_end = max(t_begin, min(vis, t_begin + chunk));
+  if (!cluster && split > 0 && t_begin >= vis) return;
   if (tid == 0) {
     s_abort = 0;
     for (int s = 0; s < kDecWarps * NST; ++s) mbar_init(&bars[s], 1);
     fence_mbar_init();
   }
   __syncthreads();
-  const int tiles = t_end > t_begin ? (t_end - t_begin + kDecTile - 1) / kDecTile : 0;
+  const int tiles = (t_end - t_begin + kDecTile - 1) / kDecTile;
   const int mine = tiles > warp ? (tiles - warp + kDecWarps - 1) / kDecWarps : 0;
   const int nblk = blocks_of(t_end, A.lb);
   uint8_t* wring = ring + warp * NST * kStage;
   uint64_t* wbar = bars + warp * NST;
-  DecMeta* wmeta = meta + warp * 64;
-  int2* wids = ids + warp * 64;
+  DecMeta* wmeta = meta + warp * 2 * kDecGroup;
+  int2* wids = ids + warp * 2 * kDecGroup;
   const size_t blk_bytes = (size_t)(D << A.lb);
 
-  // block ids and scales of 32 tiles at a time, a lane each
+  // block ids and scales of kDecGroup tiles at a time, a lane each
   const auto load_group = [&](int k0) {
     const int k = k0 + lane;
-    int2 id = make_int2(-1, -1);
-    DecMeta m = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-    if (k < mine) {
-      const int t = t_begin + (warp + kDecWarps * k) * kDecTile, c0 = t >> A.lb, c1 = (t + 16) >> A.lb;
-      const int* row = A.table + (size_t)req * A.max_blocks;
-      id.x = row[c0];
-      id.y = c1 == c0 ? id.x : (c1 < nblk ? row[c1] : -2);
-      if (id.x < 0 || id.x >= A.n_blocks) { id.x = -1; record_status(SVDQ_ERR_INVALID_ARG); }
-      if (id.y != -2 && (id.y < 0 || id.y >= A.n_blocks)) { id.y = -1; record_status(SVDQ_ERR_INVALID_ARG); }
-      if (id.x >= 0) { const size_t c = (size_t)id.x * A.kv + h; m.sk[0] = A.ks[c]; m.sv[0] = A.vs[c]; }
-      if (id.y >= 0) { const size_t c = (size_t)id.y * A.kv + h; m.sk[1] = A.ks[c]; m.sv[1] = A.vs[c]; }
+    if (lane < kDecGroup) {
+      int2 id = make_int2(-1, -1);
+      DecMeta m = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+      if (k < mine) {
+        const int t = t_begin + (warp + kDecWarps * k) * kDecTile, c0 = t >> A.lb, c1 = (t + 16) >> A.lb;
+        const int* row = A.table + (size_t)req * A.max_blocks;
+        id.x = row[c0];
+        id.y = c1 == c0 ? id.x : (c1 < nblk ? row[c1] : -2);
+        if (id.x < 0 || id.x >= A.n_blocks) { id.x = -1; record_status(SVDQ_ERR_INVALID_ARG); }
+        if (id.y != -2 && (id.y < 0 || id.y >= A.n_blocks)) { id.y = -1; record_status(SVDQ_ERR_INVALID_ARG); }
+        if (id.x >= 0) { const size_t c = (size_t)id.x * A.kv + h; m.sk[0] = A.ks[c]; m.sv[0] = A.vs[c]; }
+        if (id.y >= 0) { const size_t c = (size_t)id.y * A.kv + h; m.sk[1] = A.ks[c]; m.sv[1] = A.vs[c]; }
+      }
+      wids[k & (2 * kDecGroup - 1)] = id;
+      wmeta[k & (2 * kDecGroup - 1)] = m;
     }
-    wids[k & 63] = id;
-    wmeta[k & 63] = m;
     __syncwarp();
   };
   const auto issue = [&](int k) {
-    if ((k & 31) == 0) load_group(k);
+    if ((k & (kDecGroup - 1)) == 0) load_group(k);
     if (lane == 0) {
       const int t = t_begin + (warp + kDecWarps * k) * kDecTile, o = t & ((1 << A.lb) - 1);
-      const int2 id = wids[k & 63];
+      const int2 id = wids[k & (2 * kDecGroup - 1)];
       uint8_t* dst = wring + (k % NST) * kStage;
       uint64_t* bar = &wbar[k % NST];
       if (A.lb >= 5) {
@@ -552,92 +585,138 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
   };
   for (int k = 0; k < min(mine, NST); ++k) issue(k);
 
-  load_queries<DT, D>(A, R, h, r0, 16, sq, sf, warp, kDecWarps, lane);
+  load_queries<DT, D>(A, R, h, 0, NR, sq, sf, warp, kDecWarps, lane);
   __syncthreads();
-  uint32_t qf[D / 16][4];
+  // Q^T fragments: k-step s covers d = 64 (s / 4) + 16 q4 + 4 (s % 4) + {0, 1 | 2, 3}
+  uint32_t qf[NB][D / 16][2];
+  float f[NB][2];
+  int see[NB][2];
 #pragma unroll
-  for (int s = 0; s < D / 16; ++s) {
-    const int col = (s >> 2) * 64 + q4 * 16 + 4 * (s & 3);
-    const uint2 lo = *reinterpret_cast<const uint2*>(sq + g * (D + 8) + col);
-    const uint2 hi = *reinterpret_cast<const uint2*>(sq + (g + 8) * (D + 8) + col);
-    qf[s][0] = lo.x; qf[s][1] = hi.x; qf[s][2] = lo.y; qf[s][3] = hi.y;
+  for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      const uint2 w = *reinterpret_cast<const uint2*>(sq + (nb * 8 + g) * (D + 8) + (s >> 2) * 64 + q4 * 16 + 4 * (s & 3));
+      qf[nb][s][0] = w.x;
+      qf[nb][s][1] = w.y;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = nb * 8 + 2 * q4 + i;
+      f[nb][i] = sf[r] * kUnit<FMT>;
+      see[nb][i] = r < R.rows ? min(t_end, seen_by(A, R, r)) : t_end;
+    }
   }
-  const float f0 = sf[g] * kUnit<FMT>, f1 = sf[g + 8] * kUnit<FMT>;
-  const int see0 = r0 + g < R.rows ? min(t_end, seen_by(A, R, r0 + g)) : t_end;
-  const int see1 = r0 + g + 8 < R.rows ? min(t_end, seen_by(A, R, r0 + g + 8)) : t_end;
   const int clear = min(t_end, first_vis);              // tiles that end at or below this need no mask
-  float o[NV][4];
+  float o[D / 16][NB][4], m[NB][2], l[NB][2], vref = 0.0f;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f, vref = 0.0f;
+  for (int nb = 0; nb < NB; ++nb) {
+    m[nb][0] = m[nb][1] = -INFINITY;
+    l[nb][0] = l[nb][1] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) o[j][nb][0] = o[j][nb][1] = o[j][nb][2] = o[j][nb][3] = 0.0f;
+  }
 
   for (int k = 0; k < mine; ++k) {
     const int st = k % NST, t = t_begin + (warp + kDecWarps * k) * kDecTile;
-    if (!mbar_wait(&wbar[st], (k / NST) & 1, &s_abort)) break;
+    if (!mbar_wait(&wbar[st], (k / NST) & 1, &s_abort)) {
+      int own = 0;                                       // the copies in flight end before the CTA does
+      for (int i = k; i < min(mine, k + NST); ++i) mbar_wait(&wbar[i % NST], (i / NST) & 1, &own);
+      break;
+    }
     const uint8_t* kt = wring + st * kStage;
     const uint8_t* vt = kt + kDecTile * D;
-    const DecMeta md = wmeta[k & 63];
-    const int2 id = wids[k & 63];
-    float x[4][4];
+    const DecMeta md = wmeta[k & (2 * kDecGroup - 1)];
+    const int2 id = wids[k & (2 * kDecGroup - 1)];
+    // x[mt][nb]: tokens 16 mt + g (0, 1) and + 8 (2, 3), rows 8 nb + 2 q4 + {0, 1}
+    float x[2][NB][4];
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.0f;
+    for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
-    for (int c = 0; c < KC; ++c)
+      for (int nb = 0; nb < NB; ++nb) x[mt][nb][0] = x[mt][nb][1] = x[mt][nb][2] = x[mt][nb][3] = 0.0f;
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        const uint4 w = *reinterpret_cast<const uint4*>(kt + (nt * 8 + g) * D + c * 64 + q4 * 16);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      for (int c = 0; c < KC; ++c) {
+        const uint4 lo = *reinterpret_cast<const uint4*>(kt + (mt * 16 + g) * D + c * 64 + q4 * 16);
+        const uint4 hi = *reinterpret_cast<const uint4*>(kt + (mt * 16 + g + 8) * D + c * 64 + q4 * 16);
+        const uint32_t u[4] = {lo.x, lo.y, lo.z, lo.w}, w[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t y = pre<FMT>(u[i]);
-          mma16816(x[nt], qf[c * 4 + i], half2_of<FMT, 0>(y), half2_of<FMT, 1>(y));
+          const uint32_t y = pre<FMT>(u[i]), z = pre<FMT>(w[i]);
+          const uint32_t a[4] = {half2_of<FMT, 0>(y), half2_of<FMT, 0>(z), half2_of<FMT, 1>(y), half2_of<FMT, 1>(z)};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma16816(x[mt][nb], a, qf[nb][c * 4 + i][0], qf[nb][c * 4 + i][1]);
         }
       }
+    }
     // scores in units of log2, masked
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      const float sk = md.sk[nt >> 1];
-      x[nt][0] *= f0 * sk; x[nt][1] *= f0 * sk; x[nt][2] *= f1 * sk; x[nt][3] *= f1 * sk;
-    }
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const float s0 = f[nb][0] * md.sk[mt], s1 = f[nb][1] * md.sk[mt];
+        x[mt][nb][0] *= s0; x[mt][nb][1] *= s1; x[mt][nb][2] *= s0; x[mt][nb][3] *= s1;
+      }
     if (t + kDecTile > clear || id.x < 0 || id.y < 0) {
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        const bool gone = (nt < 2 ? id.x : id.y) < 0;
-        const int tt = t + nt * 8 + 2 * q4;
-        if (gone || tt >= see0) x[nt][0] = -INFINITY;
-        if (gone || tt + 1 >= see0) x[nt][1] = -INFINITY;
-        if (gone || tt >= see1) x[nt][2] = -INFINITY;
-        if (gone || tt + 1 >= see1) x[nt][3] = -INFINITY;
+      for (int mt = 0; mt < 2; ++mt) {
+        const bool gone = (mt == 0 ? id.x : id.y) < 0;
+        const int tt = t + mt * 16 + g;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          if (gone || tt >= see[nb][0]) x[mt][nb][0] = -INFINITY;
+          if (gone || tt >= see[nb][1]) x[mt][nb][1] = -INFINITY;
+          if (gone || tt + 8 >= see[nb][0]) x[mt][nb][2] = -INFINITY;
+          if (gone || tt + 8 >= see[nb][1]) x[mt][nb][3] = -INFINITY;
+        }
       }
     }
-    float a0 = -INFINITY, a1 = -INFINITY;
+    float top[NB][2];
+    bool grow = false;
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      a0 = fmaxf(a0, fmaxf(x[nt][0], x[nt][1]));
-      a1 = fmaxf(a1, fmaxf(x[nt][2], x[nt][3]));
-    }
-    a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 1)); a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
-    a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1)); a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
-    const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1), vmax = fmaxf(vref, fmaxf(md.sv[0], md.sv[1]));
-    if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1 || vmax > vref)) {
-      const float b0 = n0 == -INFINITY ? 1.0f : ex2(m0 - n0), b1 = n1 == -INFINITY ? 1.0f : ex2(m1 - n1);
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float a = fmaxf(fmaxf(x[0][nb][i], x[0][nb][i + 2]), fmaxf(x[1][nb][i], x[1][nb][i + 2]));
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
+        top[nb][i] = fmaxf(m[nb][i], a);
+        grow = grow || top[nb][i] > m[nb][i];
+      }
+    const float vmax = fmaxf(vref, fmaxf(md.sv[0], md.sv[1]));
+    if (__any_sync(0xffffffffu, grow || vmax > vref)) {
       const float fv = vmax > 0.0f ? __fdiv_rn(vref, vmax) : 1.0f;
-      l0 *= b0; l1 *= b1;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) { o[j][0] *= b0 * fv; o[j][1] *= b0 * fv; o[j][2] *= b1 * fv; o[j][3] *= b1 * fv; }
-      m0 = n0; m1 = n1; vref = vmax;
+      for (int nb = 0; nb < NB; ++nb) {
+        float b[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          b[i] = top[nb][i] == -INFINITY ? 1.0f : ex2(m[nb][i] - top[nb][i]);
+          l[nb][i] *= b[i];
+          m[nb][i] = top[nb][i];
+          b[i] *= fv;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          o[j][nb][0] *= b[0]; o[j][nb][1] *= b[1]; o[j][nb][2] *= b[0]; o[j][nb][3] *= b[1];
+        }
+      }
+      vref = vmax;
     }
-    const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
     const float rv = vref > 0.0f ? __fdiv_rn(1.0f, vref) : 0.0f;
-    uint32_t pa[2][4];
+    uint32_t pb[2][NB][2];
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      const float wv = md.sv[nt >> 1] * rv;
-      const float p0 = ex2(x[nt][0] - z0), p1 = ex2(x[nt][1] - z0), p2 = ex2(x[nt][2] - z1), p3 = ex2(x[nt][3] - z1);
-      l0 += p0 + p1;
-      l1 += p2 + p3;
-      pa[nt >> 1][(nt & 1) * 2] = pack_half2(p0 * wv, p1 * wv);
-      pa[nt >> 1][(nt & 1) * 2 + 1] = pack_half2(p2 * wv, p3 * wv);
+    for (int nb = 0; nb < NB; ++nb) {
+      const float z0 = m[nb][0] == -INFINITY ? 0.0f : m[nb][0], z1 = m[nb][1] == -INFINITY ? 0.0f : m[nb][1];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const float wv = md.sv[mt] * rv;
+        const float p0 = ex2(x[mt][nb][0] - z0), p1 = ex2(x[mt][nb][1] - z1);
+        const float p2 = ex2(x[mt][nb][2] - z0), p3 = ex2(x[mt][nb][3] - z1);
+        l[nb][0] += p0 + p2;
+        l[nb][1] += p1 + p3;
+        // [token][row] -> [row][token]: the column operand of the second product
+        pb[mt][nb][0] = transpose8x8(pack_half2(p0 * wv, p1 * wv));
+        pb[mt][nb][1] = transpose8x8(pack_half2(p2 * wv, p3 * wv));
+      }
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -653,70 +732,110 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
           u[r][0] = pre<FMT>(w.x); u[r][1] = pre<FMT>(w.y);
         }
       }
+      // accumulator tile j: operand row n is d = (D / 8) n + 2 j, row n + 8 the d after it
 #pragma unroll
       for (int w = 0; w < VW; ++w) {
         const uint32_t la = __byte_perm(u[0][w], u[1][w], 0x5140), ha = __byte_perm(u[0][w], u[1][w], 0x7362);
         const uint32_t lb = __byte_perm(u[2][w], u[3][w], 0x5140), hb = __byte_perm(u[2][w], u[3][w], 0x7362);
-        mma16816(o[4 * w + 0], pa[s], half2_of<FMT, 0>(la), half2_of<FMT, 0>(lb));
-        mma16816(o[4 * w + 1], pa[s], half2_of<FMT, 1>(la), half2_of<FMT, 1>(lb));
-        mma16816(o[4 * w + 2], pa[s], half2_of<FMT, 0>(ha), half2_of<FMT, 0>(hb));
-        mma16816(o[4 * w + 3], pa[s], half2_of<FMT, 1>(ha), half2_of<FMT, 1>(hb));
+        const uint32_t a0[4] = {half2_of<FMT, 0>(la), half2_of<FMT, 1>(la), half2_of<FMT, 0>(lb), half2_of<FMT, 1>(lb)};
+        const uint32_t a1[4] = {half2_of<FMT, 0>(ha), half2_of<FMT, 1>(ha), half2_of<FMT, 0>(hb), half2_of<FMT, 1>(hb)};
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          mma16816(o[2 * w][nb], a0, pb[s][nb][0], pb[s][nb][1]);
+          mma16816(o[2 * w + 1][nb], a1, pb[s][nb][0], pb[s][nb][1]);
+        }
       }
     }
     __syncwarp();
     if (k + NST < mine) issue(k + NST);
   }
   // join the four warps: weights 2^(m_w - M) and the value reference of each
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 1); l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 1); l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-  if (q4 == 0) { wml[warp * 16 + g] = make_float2(m0, l0); wml[warp * 16 + g + 8] = make_float2(m1, l1); }
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int s = 4; s < 32; s <<= 1) l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], s);
+      if (g == 0) wml[warp * NR + nb * 8 + 2 * q4 + i] = make_float2(m[nb][i], l[nb][i]);
+    }
   if (lane == 0) s_vref[warp] = vref * kUnit<FMT>;
   __syncthreads();                                       // every ring is free: the accumulators go there
-  float* acc = reinterpret_cast<float*>(ring);           // [warp][16][D]
-  const auto weight = [&](int w, int r, float M) { const float m = wml[w * 16 + r].x; return m == -INFINITY ? 0.0f : ex2(m - M); };
-  {
-    float M0 = -INFINITY, M1 = -INFINITY;
+  constexpr int AP = D + 4;                              // row pitch of the accumulators
+  float* acc = reinterpret_cast<float*>(ring);           // [warp][NR][AP]
+  float* mine_o = acc + kDecWarps * NR * AP;             // [NR][D]: this CTA's joined rows
+  float2* mine_ml = reinterpret_cast<float2*>(mine_o + NR * D);
+  static_assert((kDecWarps * NR * AP + NR * D + 2 * NR) * 4 <= dec_ring_bytes(D), "the join fits the ring");
+  const auto weight = [&](int w, int r, float M) { const float x = wml[w * NR + r].x; return x == -INFINITY ? 0.0f : ex2(x - M); };
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) { M0 = fmaxf(M0, wml[w * 16 + g].x); M1 = fmaxf(M1, wml[w * 16 + g + 8].x); }
-    const float w0 = weight(warp, g, M0) * s_vref[warp], w1 = weight(warp, g + 8, M1) * s_vref[warp];
-    // tile j, columns n = 2 q4, 2 q4 + 1: d = (D / 8) n + j
+  for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float* p0 = acc + (warp * 16 + g) * D + (D / 8) * 2 * q4 + j;
-      float* p1 = p0 + 8 * D;
-      p0[0] = o[j][0] * w0; p0[D / 8] = o[j][1] * w0;
-      p1[0] = o[j][2] * w1; p1[D / 8] = o[j][3] * w1;
+    for (int i = 0; i < 2; ++i) {
+      const int r = nb * 8 + 2 * q4 + i;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, wml[w * NR + r].x);
+      const float wt = weight(warp, r, M) * s_vref[warp];
+      float* p = acc + (warp * NR + r) * AP + (D / 8) * g;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+        *reinterpret_cast<float2*>(p + 2 * j) = make_float2(o[j][nb][i] * wt, o[j][nb][i + 2] * wt);
     }
-  }
   __syncthreads();
-  const bool whole = vis <= A.chunk;                     // this split holds all that the rows see
-  for (int idx = tid; idx < 16 * D / 4; idx += kDecWarps * 32) {
+  const bool whole = !cluster && vis <= chunk;           // this CTA holds all that the rows see
+  for (int idx = tid; idx < NR * D / 4; idx += kDecWarps * 32) {
     const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
-    if (r0 + r >= R.rows) break;
+    if (r >= R.rows) break;
     float M = -INFINITY, L = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, wml[w * 16 + r].x);
+    for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, wml[w * NR + r].x);
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) L += weight(w, r, M) * wml[w * 16 + r].y;
+    for (int w = 0; w < kDecWarps; ++w) L += weight(w, r, M) * wml[w * NR + r].y;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
-      const float4 y = *reinterpret_cast<const float4*>(acc + (w * 16 + r) * D + d);
+      const float4 y = *reinterpret_cast<const float4*>(acc + (w * NR + r) * AP + d);
       v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
     }
-    const int token = R.a + (r0 + r) / A.G, head = h * A.G + (r0 + r) % A.G;
-    if (whole) {
-      const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
-      uint2 w;
-      w.x = (uint32_t)store16<DT>(v.x * inv) | ((uint32_t)store16<DT>(v.y * inv) << 16);
-      w.y = (uint32_t)store16<DT>(v.z * inv) | ((uint32_t)store16<DT>(v.w * inv) << 16);
-      *reinterpret_cast<uint2*>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + d) = w;
+    const int token = R.a + r / A.G, head = h * A.G + r % A.G;
+    if (cluster) {
+      *reinterpret_cast<float4*>(mine_o + r * D + d) = v;
+      if (d == 0) mine_ml[r] = make_float2(M, L);
+    } else if (whole) {
+      store_row4<DT>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + d, v, L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f);
     } else {
       const size_t cell = ((size_t)split * A.n_tokens + token) * A.heads + head;
       *reinterpret_cast<float4*>(A.part_o + cell * D + d) = v;
       if (d == 0) *reinterpret_cast<float2*>(A.part_ml + cell * 2) = make_float2(M, L);
     }
   }
+  if (!cluster) return;
+  // the cluster's CTAs in rank order, each taking its share of the values
+  cluster_sync();
+  const uint32_t o_at = smem_u32(mine_o), ml_at = smem_u32(mine_ml);
+  for (int idx = split * (kDecWarps * 32) + tid; idx < NR * D / 4; idx += A.splits * kDecWarps * 32) {
+    const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
+    if (r >= R.rows) break;
+    float2 ml[kMaxCluster];
+    float M = -INFINITY, L = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int s = 0; s < kMaxCluster; ++s) {
+      ml[s] = s < A.splits ? ld_cluster_f32x2(mapa_shared(ml_at + 8 * r, s)) : make_float2(-INFINITY, 0.0f);
+      M = fmaxf(M, ml[s].x);
+    }
+#pragma unroll
+    for (int s = 0; s < kMaxCluster; ++s) {
+      if (s < A.splits) {
+        const float w = ml[s].x == -INFINITY ? 0.0f : ex2(ml[s].x - M);
+        const float4 y = ld_cluster_f32x4(mapa_shared(o_at + (r * D + d) * 4, s));
+        L += w * ml[s].y;
+        v.x += w * y.x; v.y += w * y.y; v.z += w * y.z; v.w += w * y.w;
+      }
+    }
+    const int token = R.a + r / A.G, head = h * A.G + r % A.G;
+    store_row4<DT>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + d, v, L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f);
+  }
+  cluster_sync();                                        // nobody leaves while its rows are read
 }
 
 // Many rows: 128 or 256 rows of one (request, kv head) against a range of its
@@ -784,7 +903,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
   TileMeta* meta = reinterpret_cast<TileMeta*>(sf + 256);  // [kTileMeta][8]
   uint64_t* bars = reinterpret_cast<uint64_t*>(meta + kTileMeta * 8);
   uint64_t *k_full = bars, *k_empty = bars + 2, *v_full = bars + 4, *v_empty = bars + 6, *s_full = bars + 8,
-           *p_full = bars + 10, *o_full = bars + 12;
+           *p_full = bars + 10, *o_full = bars + 12, *drained = bars + 14;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ float s_ref;
@@ -822,6 +941,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
       mbar_init(&p_full[s], 128);
       mbar_init(&o_full[s], 1);
     }
+    mbar_init(drained, 1);
     fence_mbar_init();
   }
   if (warp == 12) {
@@ -1112,6 +1232,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
         mma_commit(&v_empty[j & 1]);
         if (j + 1 < tiles) mma_commit(&k_empty[(j + 1) & 1]);
       }
+      if (!ok) {                                         // gave up: the MMAs in flight end before TMEM is freed
+        int own = 0;
+        mma_commit(drained);
+        mbar_wait(drained, 0, &own);
+      }
     }
     __syncwarp();
   }
@@ -1123,12 +1248,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
   }
 }
 
-// Joins the splits of a row in their order: one warp per row, rows whose tokens
-// fitted one split were written already.
+// Joins the splits of a row in a fixed order: a CTA per row, warp w takes splits w,
+// w + 4, ..., then the warps in order.  Rows whose tokens fitted one split were
+// written already.
 constexpr int kJoinWarps = 4;
 template <int DT, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnArgs A, int tile_rows) {
-  const int lane = threadIdx.x & 31, r = blockIdx.x * kJoinWarps + (threadIdx.x >> 5), h = blockIdx.y, req = blockIdx.z;
+  constexpr int V = D / 32;                              // values a lane
+  __shared__ float s_v[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.x, h = blockIdx.y, req = blockIdx.z;
   griddep_wait();
   const Rows R = request_rows(A, req);
   if (r >= R.rows) return;
@@ -1137,26 +1265,50 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnA
   const int n = (vis + A.chunk - 1) / A.chunk;
   const int token = R.a + r / A.G, head = h * A.G + r % A.G;
   const size_t cell = (size_t)token * A.heads + head, step = (size_t)A.n_tokens * A.heads;
-  float M = -INFINITY;
-  for (int s = lane; s < n; s += 32) M = fmaxf(M, A.part_ml[(cell + s * step) * 2]);
+  float m = -INFINITY, l = 0.0f, v[V];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.0f, v[D / 32];
+  for (int k = 0; k < V; ++k) v[k] = 0.0f;
+  for (int s0 = warp; s0 < n; s0 += 8 * kJoinWarps) {
+    float2 ml[8];
+    float x[8][V], top = m;
 #pragma unroll
-  for (int k = 0; k < D / 32; ++k) v[k] = 0.0f;
-#pragma unroll 4
-  for (int s = 0; s < n; ++s) {
-    const size_t c = cell + s * step;
-    const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + c * 2);
-    const float w = ml.x == -INFINITY ? 0.0f : ex2(ml.x - M);
-    L += w * ml.y;
+    for (int i = 0; i < 8; ++i) {
+      const int s = s0 + i * kJoinWarps;
+      const size_t c = cell + (size_t)s * step;
+      ml[i] = s < n ? *reinterpret_cast<const float2*>(A.part_ml + c * 2) : make_float2(-INFINITY, 0.0f);
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) v[k] += w * A.part_o[c * D + lane + 32 * k];
+      for (int k = 0; k < V; ++k) x[i][k] = s < n ? A.part_o[c * D + V * lane + k] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, ml[i].x);
+    const float b = m == -INFINITY ? 0.0f : ex2(m - top);
+    m = top;
+    l *= b;
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] *= b;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float w = ml[i].x == -INFINITY ? 0.0f : ex2(ml[i].x - m);
+      l += w * ml[i].y;
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[k] += w * x[i][k];
+    }
   }
-  const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
+  if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
 #pragma unroll
-  for (int k = 0; k < D / 32; ++k)
-    A.out[(int64_t)token * A.out_stride + (int64_t)head * D + lane + 32 * k] = store16<DT>(v[k] * inv);
+  for (int k = 0; k < V; ++k) s_v[warp][V * lane + k] = v[k];
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  float M = -INFINITY, L = 0.0f, y = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_m[w]);
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float b = s_m[w] == -INFINITY ? 0.0f : ex2(s_m[w] - M);
+    L += b * s_l[w];
+    y += b * s_v[w][threadIdx.x];
+  }
+  A.out[(int64_t)token * A.out_stride + (int64_t)head * D + threadIdx.x] = store16<DT>(L > 0.0f ? __fdiv_rn(y, L) : 0.0f);
 }
 
 // ------------------------------------------------------------- host launchers
@@ -1203,11 +1355,12 @@ struct Device { std::atomic<int> state; int sms; };   // state: 0 unknown, 1 rea
 Device g_devices[64];
 
 template <int DT, int FMT, int D>
-cudaError_t rows_attr() {
-  const cudaError_t e =
-      cudaFuncSetAttribute(paged_rows_kernel<DT, FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dec_smem(D));
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(paged_tiles_kernel<DT, FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, tiles_smem(D));
+cudaError_t attention_attr() {
+  const auto smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<DT, FMT, D, 1>, smem, dec_smem(D, 1));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_rows_kernel<DT, FMT, D, 2>, smem, dec_smem(D, 2));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_tiles_kernel<DT, FMT, D>, smem, tiles_smem(D));
+  return e;
 }
 
 svdq_status device_ready(int* sms) {
@@ -1226,14 +1379,14 @@ svdq_status device_ready(int* sms) {
     if (major == 10 && minor == 0) {
       e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                plan_smem_bytes(kMaxRequests));
-      if (e == cudaSuccess) e = rows_attr<SVDQ_BF16, SVDQ_KV_INT8, 64>();
-      if (e == cudaSuccess) e = rows_attr<SVDQ_BF16, SVDQ_KV_INT8, 128>();
-      if (e == cudaSuccess) e = rows_attr<SVDQ_BF16, SVDQ_KV_E4M3, 64>();
-      if (e == cudaSuccess) e = rows_attr<SVDQ_BF16, SVDQ_KV_E4M3, 128>();
-      if (e == cudaSuccess) e = rows_attr<SVDQ_F16, SVDQ_KV_INT8, 64>();
-      if (e == cudaSuccess) e = rows_attr<SVDQ_F16, SVDQ_KV_INT8, 128>();
-      if (e == cudaSuccess) e = rows_attr<SVDQ_F16, SVDQ_KV_E4M3, 64>();
-      if (e == cudaSuccess) e = rows_attr<SVDQ_F16, SVDQ_KV_E4M3, 128>();
+      if (e == cudaSuccess) e = attention_attr<SVDQ_BF16, SVDQ_KV_INT8, 64>();
+      if (e == cudaSuccess) e = attention_attr<SVDQ_BF16, SVDQ_KV_INT8, 128>();
+      if (e == cudaSuccess) e = attention_attr<SVDQ_BF16, SVDQ_KV_E4M3, 64>();
+      if (e == cudaSuccess) e = attention_attr<SVDQ_BF16, SVDQ_KV_E4M3, 128>();
+      if (e == cudaSuccess) e = attention_attr<SVDQ_F16, SVDQ_KV_INT8, 64>();
+      if (e == cudaSuccess) e = attention_attr<SVDQ_F16, SVDQ_KV_INT8, 128>();
+      if (e == cudaSuccess) e = attention_attr<SVDQ_F16, SVDQ_KV_E4M3, 64>();
+      if (e == cudaSuccess) e = attention_attr<SVDQ_F16, SVDQ_KV_E4M3, 128>();
       if (e != cudaSuccess) return cuda_failure(e, "paged cache kernel attributes");
       state = 1;
     } else {
@@ -1255,52 +1408,75 @@ svdq_status launched(const char* where) {
 // for without a device.
 constexpr int kSplitSms = 148;
 
-// How a call's rows and tokens are split: CTAs of `cta_rows` rows (16: the few-row
-// kernel, 128 or 256: the tensor-core kernel) x `splits` ranges of `chunk` tokens (a
-// multiple of 128).
-struct Split { int cta_rows, row_ctas, splits, chunk; };
+// How a call's rows and tokens are split: CTAs of `cta_rows` rows (8, 16: the few-row
+// kernel; 128, 256: the tensor-core kernel) x `splits` ranges of tokens.  Up to
+// kMaxCluster splits of the few-row kernel form a cluster, which shares each
+// request's tokens evenly and joins in shared memory; otherwise a split is `chunk`
+// tokens (a multiple of 128) and a second kernel joins them through the workspace.
+struct Split { int cta_rows, row_ctas, splits, chunk, cluster; };
 Split split_of(const svdq_paged_cache* c, const svdq_paged_batch* b, int sms) {
   Split s;
   const int64_t rows = (int64_t)b->max_new * (c->heads / c->kv_heads), cells = (int64_t)b->B * c->kv_heads;
   const auto ctas = [&](int per) { return (rows + per - 1) / per * cells; };
-  int64_t target;                                   // CTAs wanted
-  int64_t least;                                    // tokens a split is worth
+  const int64_t len = std::max(b->max_len, 1);
   if (rows <= 16) {
-    s.cta_rows = 16; target = 4 * sms; least = kDecWarps * kDecTile;
-  } else {
-    s.cta_rows = ctas(256) >= sms || rows <= 128 ? (rows <= 128 ? 128 : 256) : 128;
-    target = sms; least = 1024;
+    s.cta_rows = rows <= 8 ? 8 : 16;
+    s.row_ctas = 1;
+    const int64_t unit = kDecWarps * kDecTile, want = std::min((4 * sms + cells - 1) / cells, (len + 2 * unit - 1) / (2 * unit));
+    s.cluster = want > 1 && want <= kMaxCluster;
+    s.splits = s.cluster ? (want > 4 ? 8 : want > 2 ? 4 : 2) : (int)std::max<int64_t>(1, want);
+    s.chunk = (int)(((len + s.splits - 1) / s.splits + unit - 1) / unit * unit);
+    if (!s.cluster) s.splits = (int)((len + s.chunk - 1) / s.chunk);
+    return s;
   }
+  s.cta_rows = rows > 128 && ctas(256) >= sms ? 256 : 128;
   s.row_ctas = (int)((rows + s.cta_rows - 1) / s.cta_rows);
-  const int64_t len = std::max(b->max_len, 1), n = ctas(s.cta_rows);
-  const int64_t want = std::max<int64_t>(1, std::min((target + n - 1) / n, (len + least - 1) / least));
-  s.chunk = (int)(((len + want - 1) / want + 127) / 128 * 128);
+  s.cluster = 0;
+  const int64_t n = ctas(s.cta_rows), want = std::max<int64_t>(1, std::min((sms + n - 1) / n, (len + 1023) / 1024));
+  s.chunk = (int)(((len + want - 1) / want + kTileTok - 1) / kTileTok * kTileTok);
   s.splits = (int)((len + s.chunk - 1) / s.chunk);
   return s;
 }
 
 size_t attention_ws(const svdq_paged_cache* c, const svdq_paged_batch* b) {
   const Split s = split_of(c, b, kSplitSms);
-  if (s.splits <= 1) return 16;
+  if (s.splits <= 1 || s.cluster) return 16;
   return (size_t)s.splits * b->n_tokens * c->heads * (size_t)(c->head_dim + 2) * sizeof(float);
+}
+
+template <int DT, int FMT, int D, int NB>
+cudaError_t launch_rows(const AttnArgs& A, const Split& s, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)s.splits, (unsigned)A.kv, (unsigned)A.B);
+  cfg.blockDim = dim3(kDecWarps * 32);
+  cfg.dynamicSmemBytes = dec_smem(D, NB);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)(s.cluster ? s.splits : 1);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_rows_kernel<DT, FMT, D, NB>, A, s.cluster);
 }
 
 template <int DT, int FMT, int D>
 svdq_status launch_attention(const AttnArgs& A, const Split& s, cudaStream_t stream) {
-  svdq_status st;
-  if (s.cta_rows == 16) {
-    const dim3 grid((unsigned)s.splits, (unsigned)(A.kv * s.row_ctas), (unsigned)A.B);
-    paged_rows_kernel<DT, FMT, D><<<grid, kDecWarps * 32, dec_smem(D), stream>>>(A);
-    st = launched("paged_rows_kernel launch");
+  cudaError_t e;
+  if (s.cta_rows <= 16) {
+    e = s.cta_rows == 8 ? launch_rows<DT, FMT, D, 1>(A, s, stream) : launch_rows<DT, FMT, D, 2>(A, s, stream);
+    if (e != cudaSuccess) return cuda_failure(e, "paged_rows_kernel launch");
   } else {
     const int64_t grid = (int64_t)s.splits * s.row_ctas * A.B * A.kv;
     if (grid > INT32_MAX) return SVDQ_ERR_UNSUPPORTED;
     paged_tiles_kernel<DT, FMT, D><<<(unsigned)grid, kTileThreads, tiles_smem(D), stream>>>(A, s.cta_rows);
-    st = launched("paged_tiles_kernel launch");
+    const svdq_status st = launched("paged_tiles_kernel launch");
+    if (st != SVDQ_OK) return st;
   }
-  if (st != SVDQ_OK || s.splits <= 1) return st;
+  if (s.splits <= 1 || s.cluster) return SVDQ_OK;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((A.max_new * A.G + kJoinWarps - 1) / kJoinWarps), (unsigned)A.kv, (unsigned)A.B);
+  cfg.gridDim = dim3((unsigned)(A.max_new * A.G), (unsigned)A.kv, (unsigned)A.B);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -1308,9 +1484,8 @@ svdq_status launch_attention(const AttnArgs& A, const Split& s, cudaStream_t str
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_join_kernel<DT, D>, A, s.cta_rows);
-  if (e != cudaSuccess) return cuda_failure(e, "paged_join_kernel launch");
-  return launched("paged_join_kernel launch");
+  e = cudaLaunchKernelEx(&cfg, paged_join_kernel<DT, D>, A, s.cta_rows);
+  return e == cudaSuccess ? SVDQ_OK : cuda_failure(e, "paged_join_kernel launch");
 }
 
 template <int DT, int FMT, int D>
