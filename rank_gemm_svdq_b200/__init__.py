@@ -293,11 +293,20 @@ def _expect(ok: bool, what: str):
         raise SVDQError(ERR_INVALID_ARG, what)
 
 
-def _words(t, n: int, name: str) -> int:
-    """Address of a contiguous int32 tensor of at least n values."""
+def _words(t, n: int, name: str, device: int) -> int:
+    """Address of a contiguous int32 tensor of at least n values on `device`."""
     import torch
-    _expect(t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= n, f"{name}: contiguous int32, {n} values")
+    if t.dtype is not torch.int32 or t.numel() < n or t.get_device() != device or not t.is_contiguous():
+        raise SVDQError(ERR_INVALID_ARG, f"{name}: contiguous int32, {n} values, device {device}")
     return t.data_ptr()
+
+
+def _launch_stream(device: int, stream) -> int | None:
+    """The stream of a call on buffers of `device`, which has to be the current one (None: torch's current stream)."""
+    import torch
+    if device < 0 or device != torch.cuda.current_device():
+        raise SVDQError(ERR_INVALID_ARG, f"buffers on device {device}, which is not the current one")
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def paged_cache(heads: int, kv_heads: int, head_dim: int, block_size: int, n_blocks: int, fmt: str, dtype: str,
@@ -306,10 +315,11 @@ def paged_cache(heads: int, kv_heads: int, head_dim: int, block_size: int, n_blo
     block_size x head_dim bytes, scales n_blocks x kv_heads fp32.  Keeps the tensors alive."""
     c = svdq_paged_cache(None, None, None, None, heads, kv_heads, head_dim, block_size, n_blocks, KV_FMT[fmt],
                          DTYPE[dtype], 0)
-    cells = n_blocks * kv_heads
+    cells, c.device = n_blocks * kv_heads, kcodes.get_device()
     for name, t, n in (("kcodes", kcodes, cells * block_size * head_dim), ("vcodes", vcodes, cells * block_size * head_dim),
                        ("kscale", kscale, 4 * cells), ("vscale", vscale, 4 * cells)):
         _expect(t.is_contiguous() and t.numel() * t.element_size() >= n, f"paged_cache: {name}, contiguous, {n} bytes")
+        _expect(t.get_device() == c.device, f"paged_cache: {name} on device {c.device}")
         setattr(c, name, t.data_ptr())
     c.tensors, c.ref = (kcodes, kscale, vcodes, vscale), ctypes.addressof(c)
     c.q_cols, c.kv_cols = heads * head_dim, kv_heads * head_dim
@@ -322,41 +332,52 @@ def paged_batch(table, lens, cu, slots=None, *, max_new: int, max_len: int,
     None for attention alone, with n_tokens given).  max_new and max_len bound the requests' new tokens and
     cached lengths.  Keeps the tensors alive."""
     B, max_blocks = table.shape
-    n = slots.numel() if n_tokens is None else n_tokens
-    _expect(n_tokens is None or slots is None or slots.numel() >= n, "paged_batch: slots")
-    b = svdq_paged_batch(_words(table, B * max_blocks, "table"), _words(lens, B, "lens"), _words(cu, B + 1, "cu"),
-                         None if slots is None else _words(slots, n, "slots"), B, max_blocks, n, max_new, max_len, 0)
-    b.tensors, b.ref = (table, lens, cu, slots), ctypes.addressof(b)
+    _expect(slots is not None or n_tokens is not None, "paged_batch: n_tokens, where there are no slots")
+    n, device = slots.numel() if n_tokens is None else n_tokens, table.get_device()
+    b = svdq_paged_batch(_words(table, B * max_blocks, "table", device), _words(lens, B, "lens", device),
+                         _words(cu, B + 1, "cu", device), None if slots is None else _words(slots, n, "slots", device),
+                         B, max_blocks, n, max_new, max_len, 0)
+    b.tensors, b.device, b.ref = (table, lens, cu, slots), device, ctypes.addressof(b)
     return b
 
 
 def paged_plan(batch: svdq_paged_batch, block_size: int, prev, target, ring, state_in, state_out, stream=None):
     """Lengths prev -> target (device int32, B each): takes blocks from the free ring or gives them back and
     writes the batch's table, lens, cu and slots; state_out = {head, count, lacking, new tokens}."""
-    _check(_lib.svdq_paged_plan(batch.ref, block_size, ring.numel(), _words(prev, batch.B, "prev"),
-                                _words(target, batch.B, "target"), _words(ring, 1, "ring"),
-                                _words(state_in, 4, "state_in"), _words(state_out, 4, "state_out"),
-                                _stream(stream)), "svdq_paged_plan")
+    B, dev = batch.B, batch.device
+    st = _lib.svdq_paged_plan(batch.ref, block_size, ring.numel(), _words(prev, B, "prev", dev),
+                              _words(target, B, "target", dev), _words(ring, 1, "ring", dev),
+                              _words(state_in, 4, "state_in", dev), _words(state_out, 4, "state_out", dev),
+                              _launch_stream(dev, stream))
+    _check(st, "svdq_paged_plan")
 
 
-def _rows16(t, n: int, cols: int, dtype: int, name: str) -> tuple[int, int]:
+def _rows16(t, n: int, cols: int, cache: svdq_paged_cache, name: str) -> tuple[int, int]:
     """Address and row stride (elements) of n rows of `cols` values (any trailing shape, contiguous in a row)."""
     import torch
-    ok = t.dtype == (torch.bfloat16 if dtype == BF16 else torch.float16) and t.shape[0] >= n
-    if t.dim() == 2:
-        ok = ok and t.shape[1] == cols and t.stride(1) == 1
-    else:
-        ok = ok and t.dim() == 3 and t.shape[1] * t.shape[2] == cols and t.stride(2) == 1 and \
-            (t.shape[1] == 1 or t.stride(1) == t.shape[2])
-    _expect(ok, f"{name}: {n} rows of {cols} values in the cache's dtype, contiguous within a row")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(cols, t.stride(0)))
+    shape, ok = t.shape, False
+    if t.dtype is (torch.bfloat16 if cache.dtype == BF16 else torch.float16) and t.get_device() == cache.device:
+        if len(shape) == 2:
+            stride, one = t.stride()
+            ok = shape[1] == cols and one == 1
+        elif len(shape) == 3:
+            stride, head, one = t.stride()
+            ok = shape[1] * shape[2] == cols and one == 1 and (shape[1] == 1 or head == shape[2])
+    if not ok or shape[0] < n:
+        raise SVDQError(ERR_INVALID_ARG, f"{name}: {n} rows of {cols} values in the cache's dtype and on its device, "
+                                         "contiguous within a row")
+    return t.data_ptr(), stride if shape[0] > 1 else max(cols, stride)
 
 
 def paged_append(cache: svdq_paged_cache, batch: svdq_paged_batch, K, V, stream=None):
     """Quantises the step's keys and values (n_tokens rows of kv_heads x head_dim, row strides free) into the cache."""
-    k, ks = _rows16(K, batch.n_tokens, cache.kv_cols, cache.dtype, "K")
-    v, vs = _rows16(V, batch.n_tokens, cache.kv_cols, cache.dtype, "V")
-    _check(_lib.svdq_paged_append(cache.ref, batch.ref, k, ks, v, vs, _stream(stream)), "svdq_paged_append")
+    n, cols = batch.n_tokens, cache.kv_cols
+    k, ks = _rows16(K, n, cols, cache, "K")
+    v, vs = _rows16(V, n, cols, cache, "V")
+    if batch.device != cache.device:
+        raise SVDQError(ERR_INVALID_ARG, "cache and batch on different devices")
+    st = _lib.svdq_paged_append(cache.ref, batch.ref, k, ks, v, vs, _launch_stream(cache.device, stream))
+    _check(st, "svdq_paged_append")
 
 
 def paged_attention_workspace_bytes(cache: svdq_paged_cache, batch: svdq_paged_batch) -> int:
@@ -367,12 +388,15 @@ def paged_attention(cache: svdq_paged_cache, batch: svdq_paged_batch, Q, out, wo
                     scale: float | None = None, stream=None):
     """Attention of the step's queries (n_tokens rows of heads x head_dim) over the cache into out (as Q);
     scale None: 1 / sqrt(head_dim)."""
-    q, qs = _rows16(Q, batch.n_tokens, cache.q_cols, cache.dtype, "Q")
-    o, os_ = _rows16(out, batch.n_tokens, cache.q_cols, cache.dtype, "out")
-    _check(_lib.svdq_paged_attention(cache.ref, batch.ref, q, qs, int(bool(causal)),
-                                     cache.head_dim ** -0.5 if scale is None else scale, o, os_, workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _stream(stream)),
-           "svdq_paged_attention")
+    n, cols, dev = batch.n_tokens, cache.q_cols, cache.device
+    q, qs = _rows16(Q, n, cols, cache, "Q")
+    o, os_ = _rows16(out, n, cols, cache, "out")
+    if batch.device != dev or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise SVDQError(ERR_INVALID_ARG, "cache, batch and a contiguous workspace on one device")
+    st = _lib.svdq_paged_attention(cache.ref, batch.ref, q, qs, 1 if causal else 0,
+                                   cache.head_dim ** -0.5 if scale is None else scale, o, os_, workspace.data_ptr(),
+                                   workspace.nbytes, _launch_stream(dev, stream))
+    _check(st, "svdq_paged_attention")
 
 
 def linear_noalloc(p: svdq_params, blob_dev, X, M: int, Y, stream=None):

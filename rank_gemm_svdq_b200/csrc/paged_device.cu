@@ -9,6 +9,8 @@
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <float.h>
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -358,24 +360,27 @@ struct AttnArgs {
   const int* table;
   const int* lens;
   const int* cu;
-  float* part_o;           // [splits][n_tokens][heads][d]
-  float* part_ml;          // [splits][n_tokens][heads][2]
+  float* part_o;           // [splits][n_tokens][heads][d]; many rows: [CTA][2][256][d]
+  float* part_ml;          // [splits][n_tokens][heads][2]; many rows: [CTA][2][256][2]
+  struct Piece* pieces;    // many rows: [CTA][2]
   int64_t q_stride, out_stride;
   int B, max_blocks, n_tokens, max_new, max_len, n_blocks, heads, kv, G, lb, causal, splits, chunk;
   float scale_log2;
+  double inv_parts;        // 1 / CTAs of the schedule
+  uint32_t g_inv;          // ceil(2^32 / G), 0 for G = 1: x / G is exact for x G < 2^32
 };
 
 // What one request's rows see.
 struct Rows {
   int a, n, L, rows;       // first token, new tokens, cached length, n G
 };
-__device__ __forceinline__ Rows request_rows(const AttnArgs& A, int i) {
+__device__ __forceinline__ Rows request_rows(const AttnArgs& A, int i, bool note) {
   Rows R;
   R.a = clampi(A.cu[i], 0, A.n_tokens);
   const int e = clampi(A.cu[i + 1], 0, A.n_tokens), n = e - R.a, L = A.lens[i];
   R.n = clampi(n, 0, A.max_new);
   R.L = clampi(L, 0, min(A.max_len, A.max_blocks << A.lb));
-  if (threadIdx.x == 0 && (n > A.max_new || L > R.L)) record_status(SVDQ_ERR_INVALID_ARG);
+  if (note && (n > A.max_new || L > R.L)) record_status(SVDQ_ERR_INVALID_ARG);
   R.rows = R.n * A.G;
   return R;
 }
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
   const int h = blockIdx.y, req = blockIdx.z, split = blockIdx.x;
   if (!cluster) griddep_launch();
-  const Rows R = request_rows(A, req);
+  const Rows R = request_rows(A, req, threadIdx.x == 0);
   if (R.rows == 0) return;
   const int vis = seen_by(A, R, R.rows - 1), first_vis = seen_by(A, R, 0);
   // a cluster shares what the rows see; otherwise a fixed chunk a split
@@ -838,24 +843,174 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
   cluster_sync();                                        // nobody leaves while its rows are read
 }
 
-// Many rows: 128 or 256 rows of one (request, kv head) against a range of its
-// tokens, on the tensor cores.  Codes become fp16 operands in shared memory once
-// per 128 tokens and serve both 128-row tiles: S = Q K^T (both operands from shared
-// memory, 128 x 128 fp32 in TMEM), P in fp16 over S's own columns, O += P V (P from
-// TMEM; V as it lies, token rows of 64 d, an MN-major operand).  Roles:
+// ------------------------------------------------------- balanced schedule
+// The calls' lengths are known on the device only, so every CTA works out its own
+// share.  An item is `cr` rows of one (request, kv head); its cost is what its last
+// row sees plus a tile for filling and emptying the pipeline, times G:
+//   c_r = G (P + 128) + cr (r + 1) [causal],  P = L - n (causal) or L
+// which sums in closed form over the row blocks r of a head, the heads and the
+// requests.  CTA c of N takes the costs [T c / N, T (c + 1) / N); a border inside an
+// item cuts its token tiles in proportion.  The two pieces of a cut item go to the
+// workspace and paged_join_kernel adds them; everything else is written directly.
+// Measured against a grid of (item, fixed split): six ragged prompts, whose rows see
+// 2 to 12 tiles, 283 -> 209 us; 256 equal items on 148 SMs took two full waves (782 -> 610 us).
+constexpr int kTileTok = 128, kTileRows = 256;
+struct Item {
+  int req, h, a, n, L, rows, r0, lo, hi, out;              // token tiles [lo, hi); hi < 0: no more items
+  int end[2];                                              // where the row tiles' token tiles end
+};
+enum { kItemWhole = 2 };                                   // out: 0, 1 a piece's slot in the workspace
+struct Piece { int valid, last, token, n_rows, h, r0, pad0, pad1; };
+
+__device__ __forceinline__ int64_t item_base(const AttnArgs& A, const Rows& R) {
+  return (int64_t)A.G * ((A.causal ? max(0, R.L - R.n) : R.L) + kTileTok);
+}
+__device__ __forceinline__ int64_t head_cost(const AttnArgs& A, const Rows& R, int64_t r, int cr) {   // row blocks [0, r)
+  return r * item_base(A, R) + (A.causal ? cr * (r * (r + 1) / 2) : 0);
+}
+__device__ __forceinline__ int64_t request_cost(const AttnArgs& A, const Rows& R, int cr) {
+  return R.rows == 0 ? 0 : A.kv * head_cost(A, R, (R.rows + cr - 1) / cr, cr);
+}
+
+// A CTA's range of costs and the request that holds its start.  Called by all
+// threads of the CTA; ends with a barrier.
+struct Share { long long x0, x1, at; int req; };
+template <int THREADS>
+__device__ __forceinline__ Share cta_share(const AttnArgs& A, int cr, int part, int parts) {
+  constexpr int W = THREADS / 32;
+  __shared__ long long s_sum[W];
+  __shared__ Share s_share;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const auto cost = [&](int i, bool note) { return i < A.B ? (long long)request_cost(A, request_rows(A, i, note), cr) : 0ll; };
+  const long long first = cost(tid, part == 0);
+  long long v = first;
+  for (int i = tid + THREADS; i < A.B; i += THREADS) v += cost(i, part == 0);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lane == 0) s_sum[warp] = v;
+  if (tid == 0) s_share.req = -1;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) total += s_sum[w];
+  // a border is the same number for the CTAs on its two sides, which is all that it has to be
+  const auto border = [&](int p) { return p == parts ? total : (long long)((double)total * (p * A.inv_parts)); };
+  const long long x0 = border(part), x1 = border(part + 1);
+  long long before = 0;
+  for (int i0 = 0; i0 < A.B && before <= x0; i0 += THREADS) {
+    const long long c = i0 == 0 ? first : cost(i0 + tid, false);
+    long long p = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, p, o);
+      if (lane >= o) p += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = p;
+    __syncthreads();
+    long long at = before + p - c;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) at += s_sum[w];
+      before += s_sum[w];
+    }
+    if (at <= x0 && x0 < at + c) s_share = Share{x0, x1, at, i0 + tid};
+  }
+  __syncthreads();
+  return s_share;
+}
+
+// The items of a share, one after another (by a converged warp).
+struct Walk {
+  Rows R;
+  long long s, base;                                       // cost where the present item starts
+  int req, h, r, nr;
+  __device__ __forceinline__ void enter(const AttnArgs& A, int cr) {
+    base = item_base(A, R);
+    nr = (R.rows + cr - 1) / cr;
+    h = r = 0;
+  }
+  __device__ __forceinline__ void start(const AttnArgs& A, const Share& S, int cr) {
+    req = S.req;
+    R = request_rows(A, req, false);
+    enter(A, cr);
+    const long long head = head_cost(A, R, nr, cr);
+    long long y = S.x0 - S.at;
+    h = (int)((double)y / (double)head);                   // within one of the quotient
+    h -= (long long)h * head > y;
+    h += (long long)(h + 1) * head <= y;
+    y -= h * head;
+    int hi = nr - 1;                                       // the last row block that starts at or below y
+    while (r < hi) {
+      const int mid = r + (hi - r + 1) / 2;
+      if (head_cost(A, R, mid, cr) <= y) r = mid; else hi = mid - 1;
+    }
+    s = S.at + h * head + head_cost(A, R, r, cr);
+  }
+  // The present item's part of the share, then one step on; false past the share's end.
+  __device__ __forceinline__ bool next(const AttnArgs& A, const Share& S, int cr, Item& it) {
+    while (s < S.x1) {
+      const long long c = base + (A.causal ? (long long)cr * (r + 1) : 0);
+      const int vis = seen_by(A, R, min(R.rows, (r + 1) * cr) - 1), tiles = (vis + kTileTok - 1) / kTileTok;
+      const auto cut = [&](long long x) { return min(tiles, (int)((double)(x - s) * tiles / (double)c)); };
+      const int lo = s >= S.x0 ? 0 : cut(S.x0), hi = s + c <= S.x1 ? tiles : cut(S.x1);
+      const bool mine = tiles == 0 ? s >= S.x0 : hi > lo;
+      it = Item{req, h, R.a, R.n, R.L, R.rows, r * cr, lo, hi, lo == 0 && hi == tiles ? (int)kItemWhole : (lo == 0 ? 1 : 0), {hi, lo}};
+      if (cr == kTileRows) {
+        const int first = r * cr, t0 = (seen_by(A, R, min(R.rows, first + 128) - 1) + kTileTok - 1) / kTileTok;
+        it.end[0] = max(lo, min(hi, t0));
+        if (first + 128 < R.rows) it.end[1] = hi;
+      }
+      s += c;
+      if (++r == nr) {
+        r = 0;
+        if (++h == A.kv) {
+          // the next request with rows, 32 at a time
+          uint32_t some = 0;
+          for (++req; req < A.B; req += 32) {
+            const int i = req + (threadIdx.x & 31);
+            some = __ballot_sync(0xffffffffu, i < A.B && request_rows(A, i, false).rows > 0);
+            if (some) break;
+          }
+          if (some) {
+            req += __ffs(some) - 1;
+            R = request_rows(A, req, false);
+            enter(A, cr);
+          } else {
+            s = S.x1;
+          }
+        }
+      }
+      if (mine) return true;
+    }
+    return false;
+  }
+};
+
+// Many rows: items of 256 rows (two tiles of 128) on the tensor cores, one CTA per SM
+// that works through its share without a break between items.  Codes become fp16
+// operands in shared memory once per 128 tokens and serve both row tiles: S = Q K^T
+// (both operands from shared memory, 128 x 128 fp32 in TMEM), P in fp16 over S's own
+// columns, O += P V (P from TMEM; V as it lies, token rows of 64 d, an MN-major
+// operand).  Roles:
 //   warps 0-3, 4-7   softmax of row tile 0 / 1, a row per thread: maximum, weights,
-//                    sum; rescales O only when a maximum grew by more than 2^8
-//                    (weights stay below 2^8 in fp16)
+//                    sum; rescales O only when a maximum (or the largest value scale)
+//                    grew by more than 2^7 (weights stay below 2^14 in fp16); output
 //   warps 8-11       codes -> fp16 (the next tile's codes already in registers)
+//                    of an item and, ahead of it, the queries of the next one
 //   warp 12          issues the MMAs: S0 S1 | P0V S0' | P1V S1' | ...
-// The value scale goes into a weight's exponent, p' = 2^(x - m + log2(s_v / s_ref))
-// with s_ref the largest value scale of the range, so it costs nothing per weight;
-// the row sum takes each 16 tokens' sum times s_ref / s_v.
-constexpr int kTileThreads = 512, kTileTok = 128, kTileMeta = 4;
-struct TileMeta { float sk, lsv, rsv; int gone; };        // 16 tokens: key scale, log2(s_v / s_ref), s_ref / s_v
+//   warp 13          walks the schedule, up to eight items ahead
+// The value scale goes into a weight's exponent, p' = 2^(x - m + log2 s_v - v) with v
+// the log2 of the largest value scale so far (up to 2^7), so it costs nothing per
+// weight; the row sum takes each 16 tokens' sum times 2^v / s_v.
+constexpr int kTileThreads = 512, kTileMeta = 4, kItems = 8;
+struct __align__(16) TileMeta { float sk, lsv; int gone, pad; };   // 16 tokens: key scale, log2 of the value scale
 constexpr int kTileHalf = 128 * 128;                      // 128 rows of 64 fp16, 128-byte swizzle
 constexpr int tile_bytes(int D) { return D / 64 * kTileHalf; }
-constexpr int tiles_smem(int D) { return 6 * tile_bytes(D) + 256 * 4 + kTileMeta * 8 * 16 + 128 + 1024; }
+constexpr int tiles_smem(int D) {
+  return 6 * tile_bytes(D) + kTileRows * 4 + kTileMeta * 8 * 16 + kItems * (int)sizeof(Item) + 512 + 1024;
+}
+constexpr float kGrow = 7.0f;
 
 // MN-major operand with the 128-byte swizzle: rows of 64 values (128 bytes) along K,
 // 8-row groups 1024 bytes apart, the next 64 values of MN kTileHalf further.
@@ -880,6 +1035,44 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
+// 2^d for a whole number d <= 0 (0 below the normal numbers).
+__device__ __forceinline__ float power_of_two(float d) { return __uint_as_float((uint32_t)(max((int)d, -127) + 127) << 23); }
+
+// threadIdx.x, read where it stands: what is computed from it is not kept in registers across the loops before.
+__device__ __forceinline__ int tid_here() {
+  int t;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+  return t;
+}
+
+// One lane of a converged warp; the compiler knows that the choice is uniform.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // 16 code bytes to 16 fp16 at columns 16 c .. of row r of an operand tile.
 template <int FMT>
 __device__ __forceinline__ void store_codes(uint8_t* tile, int r, int half, int c, const uint4& w) {
@@ -891,55 +1084,50 @@ __device__ __forceinline__ void store_codes(uint8_t* tile, int r, int half, int 
       make_uint4(half2_of<FMT, 0>(u[2]), half2_of<FMT, 1>(u[2]), half2_of<FMT, 0>(u[3]), half2_of<FMT, 1>(u[3]));
 }
 
+// Codes are read once by an SM: they leave L1 to the block tables and scales.
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 template <int DT, int FMT, int D>
-__global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const AttnArgs A, int cta_rows) {
-  constexpr int H = D / 64, TB = tile_bytes(D);
+__global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const AttnArgs A) {
+  constexpr int H = D / 64, TB = tile_bytes(D), kConsumers = 8 + 4 + 1;
   extern __shared__ uint8_t tsm_raw[];
   uint8_t* tsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tsm_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* sq = tsm;                                       // [2 row tiles]
   uint8_t* sk = sq + 2 * TB;                               // [2 stages]
   uint8_t* sv = sk + 2 * TB;                               // [2 stages]
   float* sf = reinterpret_cast<float*>(sv + 2 * TB);       // [256]
-  TileMeta* meta = reinterpret_cast<TileMeta*>(sf + 256);  // [kTileMeta][8]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(meta + kTileMeta * 8);
+  TileMeta* meta = reinterpret_cast<TileMeta*>(sf + kTileRows);  // [kTileMeta][8]
+  Item* items = reinterpret_cast<Item*>(meta + kTileMeta * 8);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(items + kItems);
   uint64_t *k_full = bars, *k_empty = bars + 2, *v_full = bars + 4, *v_empty = bars + 6, *s_full = bars + 8,
-           *p_full = bars + 10, *o_full = bars + 12, *drained = bars + 14;
+           *p_full = bars + 10, *o_full = bars + 12, *q_full = bars + 14, *p1_full = bars + 16,
+           *o1_full = bars + 18, *i_full = bars + 20,
+           *i_empty = i_full + kItems, *drained = i_empty + kItems;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ float s_ref;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // splits fastest, then kv heads and requests, then row CTAs: the longest rows of a prompt first
-  const int split = blockIdx.x % A.splits, cell_id = (blockIdx.x / A.splits) % (A.B * A.kv);
-  const int h = cell_id % A.kv, req = cell_id / A.kv, rts = (A.max_new * A.G + cta_rows - 1) / cta_rows;
-  const int r0 = (rts - 1 - (int)(blockIdx.x / A.splits / (A.B * A.kv))) * cta_rows;
-  griddep_launch();
-  const Rows R = request_rows(A, req);
-  if (r0 >= R.rows) return;
-  const int last = min(R.rows, r0 + cta_rows) - 1;
-  const int vis = seen_by(A, R, last);
-  const int t_begin = split * A.chunk, t_end = min(vis, t_begin + A.chunk);
-  if (split > 0 && t_begin >= vis) return;
-  const int row_tiles = last - r0 >= 128 ? 2 : 1;
-  // token tiles of a row tile: what its last row sees
-  const auto tiles_of = [&](int rt) {
-    const int e = min(t_end, seen_by(A, R, min(R.rows, r0 + rt * 128 + 128) - 1));
-    return e > t_begin ? (e - t_begin + kTileTok - 1) / kTileTok : 0;
-  };
-  const int n0 = tiles_of(0), n1 = row_tiles == 2 ? tiles_of(1) : 0, tiles = max(n0, n1);
-  const int nblk = blocks_of(t_end, A.lb);
-  const int* row = A.table + (size_t)req * A.max_blocks;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (tid == 0) {
     s_abort = 0;
-    s_ref = 0.0f;
     for (int s = 0; s < 2; ++s) {
       mbar_init(&k_full[s], 4);
       mbar_init(&k_empty[s], 1);
       mbar_init(&v_full[s], 4);
       mbar_init(&v_empty[s], 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 128);
+      mbar_init(&p_full[s], 4);
+      mbar_init(&p1_full[s], 4);
+      mbar_init(&o1_full[s], 1);
       mbar_init(&o_full[s], 1);
+      mbar_init(&q_full[s], 4);
+    }
+    for (int s = 0; s < kItems; ++s) {
+      mbar_init(&i_full[s], 1);
+      mbar_init(&i_empty[s], kConsumers);
     }
     mbar_init(drained, 1);
     fence_mbar_init();
@@ -948,297 +1136,439 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
   }
-  __syncthreads();
-  // the largest value scale of the range (scales are not negative: their bits order them)
-  {
-    float top = 0.0f;
-    for (int c = (t_begin >> A.lb) + tid; c < nblk; c += kTileThreads) {
-      const int id = row[c];
-      if (id >= 0 && id < A.n_blocks) top = fmaxf(top, A.vs[(size_t)id * A.kv + h]);
-      else record_status(SVDQ_ERR_INVALID_ARG);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) atomicMax(reinterpret_cast<int*>(&s_ref), __float_as_int(top));
-  }
-  // queries, normalised, as the A operand; 16 (8) lanes a row
-  if (warp < 8) {
-    constexpr int PER = D / 8, RPI = 32 / PER;             // lanes per row, rows per instruction
-    const int c = lane % PER;
-#pragma unroll 4
-    for (int k = 0; k < 32 / RPI; ++k) {
-      const int rr = warp * 32 + k * RPI + lane / PER, r = r0 + rr;
-      if (warp * 32 + k * RPI >= row_tiles * 128) break;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (r <= last)
-        w = __ldg(reinterpret_cast<const uint4*>(A.q + (int64_t)(R.a + r / A.G) * A.q_stride + (int64_t)(h * A.G + r % A.G) * D) + c);
-      float v[8], top = 0.0f;
-      unpack8<DT>(w, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
-#pragma unroll
-      for (int o = PER / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = clampi((int)(__float_as_uint(top) >> 23) - 127, -100, 100);
-      // the factor is kept non-negative (maxima are taken before it): a negative scale turns the query instead
-      const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), A.scale_log2);
-      uint8_t* dst = sq + (rr >> 7) * TB + (c >> 3) * kTileHalf + (rr & 127) * 128 + (((c & 7) ^ (rr & 7)) << 4);
-      *reinterpret_cast<uint4*>(dst) = make_uint4(pack_half2(v[0] * down, v[1] * down), pack_half2(v[2] * down, v[3] * down),
-                                                  pack_half2(v[4] * down, v[5] * down), pack_half2(v[6] * down, v[7] * down));
-      if (c == 0) sf[rr] = __uint_as_float((uint32_t)(127 + e) << 23) * fabsf(A.scale_log2) * kUnit<FMT>;
-    }
-    fence_proxy_async_smem();
-  }
+  griddep_wait();
+  griddep_launch();
+  const Share share = cta_share<kTileThreads>(A, kTileRows, blockIdx.x, gridDim.x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = s_tmem;
-  const float vref = s_ref;
+  // the k-th item, for one warp: false when there are no more; done with it: give_back
+  const auto take = [&](int k) {
+    return mbar_wait(&i_full[k % kItems], (k / kItems) & 1, &s_abort) && items[k % kItems].hi >= 0;
+  };
+  const auto give_back = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&i_empty[k % kItems]);
+  };
 
   if (warp < 8) {
-    regs_inc<184>();
-    const int rt = warp >> 2, n = rt == 0 ? n0 : n1;
+    regs_inc<144>();
+    const int rt = warp >> 2, rl = tid & 127;
     const uint32_t ts = tm + rt * 128 + ((uint32_t)(warp & 3) << 21), to = tm + 256 + rt * D + ((uint32_t)(warp & 3) << 21);
-    const int r = r0 + rt * 128 + (tid & 127);
-    const bool live = r <= last;
-    if (rt < row_tiles) {
-      const float f = sf[rt * 128 + (tid & 127)];
-      const int see = live ? min(t_end, seen_by(A, R, r)) : t_end;
-      const int clear = min(t_end, seen_by(A, R, r0 + rt * 128));
-      float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < n; ++j) {
-        const int t = t_begin + j * kTileTok;
-        if (!mbar_wait(&s_full[rt], j & 1, &s_abort)) break;
+    uint32_t n_s = 0, n_o = 0;                             // tiles and items of this row tile so far
+    int flat = 0;                                          // token tiles of all items so far
+    // An item's 32 rows of queries, normalised, as the A operand (16 or 8 lanes a row), and their factors.
+    // The row tile's last S of the item before is done, so the operand is free.
+    const auto queries = [&](const Item& N) {
+      constexpr int PER = D / 8, RPI = 32 / PER, NQ = 8;                // rows in flight: NQ RPI
+      if (N.end[rt] <= N.lo) return;
+      const int here = tid_here(), c = here % PER, w0 = (here & 127) / 32 * 32 + here % 32 / PER, t0 = N.r0 / A.G, x0 = N.r0 - t0 * A.G + rt * 128 + w0;
+      const uint16_t* q0 = A.q + (int64_t)(N.a + t0) * A.q_stride + (int64_t)N.h * A.G * D + 8 * c;
+      uint8_t* dst = sq + rt * TB + (c >> 3) * kTileHalf;
+#pragma unroll 1
+      for (int b0 = 0; b0 < 32; b0 += NQ * RPI) {
+      uint4 q[NQ];
+#pragma unroll
+      for (int b = 0; b < NQ; ++b) {
+        const int x = x0 + b0 + b * RPI;
+        const int dt = A.G == 1 ? x : (int)__umulhi((uint32_t)x, A.g_inv);   // x / G
+        q[b] = make_uint4(0, 0, 0, 0);
+        if (N.r0 + rt * 128 + w0 + b0 + b * RPI < N.rows) q[b] = *reinterpret_cast<const uint4*>(q0 + dt * A.q_stride + (int64_t)((x - dt * A.G) * D));
+      }
+#pragma unroll
+      for (int b = 0; b < NQ; ++b) {
+        const int rr = w0 + b0 + b * RPI;
+        float v[8], top = 0.0f;
+        unpack8<DT>(q[b], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+#pragma unroll
+        for (int o = PER / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int e = clampi((int)(__float_as_uint(top) >> 23) - 127, -100, 100);
+        // the factor is kept non-negative (maxima are taken before it): a negative scale turns the query instead
+        const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), A.scale_log2);
+        *reinterpret_cast<uint4*>(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) =
+            make_uint4(pack_half2(v[0] * down, v[1] * down), pack_half2(v[2] * down, v[3] * down),
+                       pack_half2(v[4] * down, v[5] * down), pack_half2(v[6] * down, v[7] * down));
+        if (c == 0) sf[rt * 128 + rr] = __uint_as_float((uint32_t)(127 + e) << 23) * fabsf(A.scale_log2) * kUnit<FMT>;
+      }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[rt]);
+    };
+    int k = 0;
+    bool some = take(0);
+    if (some) queries(items[0]);
+    while (some) {
+      const Item& I = items[k % kItems];
+      const int lo = I.lo, end = I.end[rt], rows = I.rows - (I.r0 + rt * 128);   // rows of this row tile
+      int see = INT_MAX, clear;
+      {
+        const Rows R = {I.a, I.n, I.L, I.rows};
+        if (rl < rows) see = seen_by(A, R, I.r0 + rt * 128 + rl);
+        clear = seen_by(A, R, I.r0 + rt * 128);
+      }
+      float m = -INFINITY, l = 0.0f, lv = -INFINITY;
+      const float f = sf[rt * 128 + rl];
+      bool ok = true;
+      for (int j = lo; j < end; ++j, ++n_s) {
+        const int t = j * kTileTok;
+        if (!(ok = mbar_wait(&s_full[rt], n_s & 1, &s_abort))) break;
         tc_fence_after();
-        uint32_t x[4][32];
+        // 64 tokens at a time, whose products start while the next 64 are worked on; both references are
+        // whole numbers, so that a growth rescales O and the sum by a power of two
+        const TileMeta* M = meta + ((flat + j - lo) & (kTileMeta - 1)) * 8;
+        uint32_t y[2][32];
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q, M += 4) {
+          const float4 M0 = reinterpret_cast<const float4*>(M)[0], M1 = reinterpret_cast<const float4*>(M)[1],
+                       M2 = reinterpret_cast<const float4*>(M)[2], M3 = reinterpret_cast<const float4*>(M)[3];
+          const auto sk_of = [&](int g) { return g == 0 ? M0.x : g == 1 ? M1.x : g == 2 ? M2.x : M3.x; };
+          const auto lsv_of = [&](int g) { return g == 0 ? M0.y : g == 1 ? M1.y : g == 2 ? M2.y : M3.y; };
+          const auto gone_of = [&](int g) { return __float_as_int(g == 0 ? M0.z : g == 1 ? M1.z : g == 2 ? M2.z : M3.z); };
+          tmem_ld_32cols(ts + 64 * q, y[0]);
+          tmem_ld_32cols(ts + 64 * q + 32, y[1]);
+          tmem_ld_wait(y[0]);
+          tmem_ld_wait(y[1]);
+          const auto at = [&](int i) { return __uint_as_float(y[i >> 5][i & 31]); };
+          if (t + 64 * q + 64 > clear || (gone_of(0) | gone_of(1) | gone_of(2) | gone_of(3))) {
+            const int lim = see - t - 64 * q;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld_32cols(ts + 32 * q, x[q]);
-        tmem_ld_wait();
-        const TileMeta* M = meta + (j & (kTileMeta - 1)) * 8;
-        float a[8];
-        int gone = 0;
+            for (int i = 0; i < 64; ++i)
+              if (i >= lim || gone_of(i >> 4)) y[i >> 5][i & 31] = __float_as_uint(-INFINITY);
+          }
+          float top = m, vtop = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < 8; ++g) { a[g] = f * M[g].sk; gone |= M[g].gone; }
-        if (t + kTileTok > clear || gone) {
+          for (int g = 0; g < 4; ++g) {                    // four chains: the unit is fast, its latency is not
+            const int i = 16 * g;
+            float t0 = fmaxf(fmaxf(at(i), at(i + 1)), at(i + 2)), t1 = fmaxf(fmaxf(at(i + 3), at(i + 4)), at(i + 5));
+            float t2 = fmaxf(fmaxf(at(i + 6), at(i + 7)), at(i + 8)), t3 = fmaxf(fmaxf(at(i + 9), at(i + 10)), at(i + 11));
+            t0 = fmaxf(fmaxf(t0, at(i + 12)), at(i + 13));
+            t1 = fmaxf(fmaxf(t1, at(i + 14)), at(i + 15));
+            // -inf stays -inf in a block of zeros
+            top = fmaxf(top, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * fmaxf(f * sk_of(g), FLT_MIN));
+            vtop = fmaxf(vtop, lsv_of(g));
+          }
+          // new references only where one grew by 2^kGrow (or is the first)
+          const bool grow = top > m + kGrow, vgrow = vtop > lv + kGrow;   // -inf: any finite one
+          if (__any_sync(0xffffffffu, grow || vgrow)) {
+            const float m1 = grow ? ceilf(top) : m, lv1 = vgrow ? ceilf(vtop) : lv;
+            const float b = m1 == m ? 1.0f : power_of_two(m - m1), bo = lv1 == lv ? b : b * power_of_two(lv - lv1);
+            l *= b;
+            m = m1;
+            lv = lv1;
+            if (j > lo || q == 1) {
+              // the first half's products of this tile may be under way
+              if (q == 1 && !(ok = mbar_wait(&o1_full[rt], n_s & 1, &s_abort))) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int e = 0; e < D / 8; ++e) {
+                uint32_t o[8];
+                tmem_ld_8cols(to + 8 * e, o);
+                tmem_ld_wait();
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const int lim = M[g].gone ? 0 : see - t - 16 * g;
+                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * bo);
+                tmem_st_8cols(to + 8 * e, o);
+              }
+            }
+          }
+          const float z = m == -INFINITY ? 0.0f : m, vz = lv == -INFINITY ? 0.0f : lv;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // a scale below 2^-60 of the largest counts as that: its values are lost beside it either way
+            const float ls0 = fmaxf(lsv_of(2 * h), vz - 60.0f) - vz, ls1 = fmaxf(lsv_of(2 * h + 1), vz - 60.0f) - vz;
+            const float a0 = fmaxf(f * sk_of(2 * h), FLT_MIN), a1 = fmaxf(f * sk_of(2 * h + 1), FLT_MIN);
+            const float r0 = ex2(-ls0), r1 = ex2(-ls1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[h][i] = __float_as_uint(ex2(fmaf(__uint_as_float(y[h][i]), i < 16 ? a0 : a1, (i < 16 ? ls0 : ls1) - z)));
+            uint32_t p[16];
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              uint32_t& y = x[g >> 1][(g & 1) * 16 + i];
-              y = __float_as_uint(i < lim ? __uint_as_float(y) * a[g] : -INFINITY);
+              const float p0 = __uint_as_float(y[h][2 * i]), p1 = __uint_as_float(y[h][2 * i + 1]);
+              p[i] = pack_half2(p0, p1);
+              sum[(i >> 3) * 2] += p0;
+              sum[(i >> 3) * 2 + 1] += p1;
             }
-            a[g] = 1.0f;
+            l = fmaf(sum[0] + sum[1], r0, fmaf(sum[2] + sum[3], r1, l));
+            tmem_st_16cols(ts + 32 * q + 16 * h, p);
           }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q == 0 ? &p1_full[rt] : &p_full[rt]);
         }
-        float top = m;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          float y[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(x[g >> 1][(g & 1) * 16 + i]);
-#pragma unroll
-          for (int w = 8; w > 0; w >>= 1)
-#pragma unroll
-            for (int i = 0; i < w; ++i) y[i] = fmaxf(y[i], y[i + w]);
-          top = fmaxf(top, y[0] * a[g]);
-        }
-        // a new reference maximum only where it grew by 2^8 (or is the first one)
-        const bool grow = top > m + 8.0f;                  // m = -inf: any finite top
-        if (__any_sync(0xffffffffu, grow)) {
-          const float b = grow ? (m == -INFINITY ? 0.0f : ex2(m - top)) : 1.0f;
-          if (grow) m = top;
-          l *= b;
-          if (j > 0) {
-#pragma unroll
-            for (int q = 0; q < D / 16; ++q) {
-              uint32_t o[16];
-              tmem_ld_16cols(to + 16 * q, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * b);
-              tmem_st_16cols(to + 16 * q, o);
-            }
-          }
-        }
-        const float z = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-        for (int g2 = 0; g2 < 4; ++g2) {
-          uint32_t p[16];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int g = 2 * g2 + k;
-            const float b = M[g].lsv - z;
-            float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float p0 = ex2(fmaf(__uint_as_float(x[g2][k * 16 + i]), a[g], b));
-              const float p1 = ex2(fmaf(__uint_as_float(x[g2][k * 16 + i + 1]), a[g], b));
-              s0 += p0;
-              s1 += p1;
-              p[k * 8 + i / 2] = pack_half2(p0, p1);
-            }
-            l = fmaf(s0 + s1, M[g].rsv, l);
-          }
-          tmem_st_16cols(ts + 16 * g2, p);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&p_full[rt]);
+        if (!ok) break;
       }
-      const bool whole = vis <= A.chunk;
-      const int token = R.a + r / A.G, head = h * A.G + r % A.G;
-      const bool ok = n == 0 || mbar_wait(&o_full[rt], 0, &s_abort);
-      tc_fence_after();
-      const size_t cell = ((size_t)split * A.n_tokens + token) * A.heads + head;
-      const float u = vref * kUnit<FMT>, mul = whole ? (l > 0.0f ? __fdiv_rn(u, l) : 0.0f) : u;
-      if (!whole && live) *reinterpret_cast<float2*>(A.part_ml + cell * 2) = make_float2(m, l);
+      if (!ok) break;
+      some = take(k + 1);
+      if (some) queries(items[(k + 1) % kItems]);
+      flat += I.hi - lo;
+      if (rows > 0) {
+      const int rl = tid_here() & 127;
+      const bool any = end > lo, live = rl < rows, whole = I.out == kItemWhole;
+      if (any) {
+        if (!mbar_wait(&o_full[rt], n_o & 1, &s_abort)) break;
+        ++n_o;
+        tc_fence_after();
+      }
+      const float u = lv == -INFINITY ? 0.0f : ex2(lv) * kUnit<FMT>, mul = whole ? (l > 0.0f ? __fdiv_rn(u, l) : 0.0f) : u;
+      const size_t cell = ((size_t)blockIdx.x * 2 + (whole ? 0 : I.out)) * kTileRows + rt * 128 + rl;
+      const int r = I.r0 + rt * 128 + rl, token = I.a + r / A.G, head = I.h * A.G + r % A.G;
+      if (!whole) *reinterpret_cast<float2*>(A.part_ml + cell * 2) = make_float2(m, l);
 #pragma unroll
-      for (int q = 0; q < D / 16; ++q) {
-        uint32_t o[16];
-        if (n > 0 && ok) {
-          tmem_ld_16cols(to + 16 * q, o);
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        if (any) {
+          tmem_ld_32cols(to + 32 * q, o);
           tmem_ld_wait();
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = 0;
+          for (int i = 0; i < 32; ++i) o[i] = 0;
         }
         if (live) {
-          float y[16];
+          float y[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(o[i]) * mul;
+          for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]) * mul;
           if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + 16 * q);
-            uint32_t w[8];
+            uint4* dst = reinterpret_cast<uint4*>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + 32 * q);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = (uint32_t)store16<DT>(y[2 * i]) | ((uint32_t)store16<DT>(y[2 * i + 1]) << 16);
-            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = (uint32_t)store16<DT>(y[8 * i + 2 * e]) | ((uint32_t)store16<DT>(y[8 * i + 2 * e + 1]) << 16);
+              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           } else {
-            float4* dst = reinterpret_cast<float4*>(A.part_o + cell * D + 16 * q);
+            float4* dst = reinterpret_cast<float4*>(A.part_o + cell * D + 32 * q);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
           }
         }
       }
+      }
+      give_back(k++);
     }
   } else if (warp < 12) {
-    regs_dec<96>();
-    const int w = warp - 8, c = lane & 3, rl = 32 * w + (lane >> 2);   // rows rl + 8 i
-    const size_t head_off = (size_t)h * (D << A.lb), blk_bytes = (size_t)A.kv * (D << A.lb);
+    regs_dec<128>();
+    const int w = warp - 8, c = lane & 3, r4 = lane >> 2;   // rows 32 w + r4 + 8 i, 16-byte columns c and c + 4
     uint4 kr[4 * H], vr[4 * H];
+    // a warp's 32 rows are two groups of 16 tokens: the tile's two block numbers are read a tile ahead of
+    // its codes, which are read a tile ahead of their use
+    struct Next { int id[2], h, o; };                      // o: row of the first group in its block
     float g_sk = 0.0f, g_sv = 0.0f;
-    int g_gone = 0, id[4];
-    const auto ids = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = (t_begin + j * kTileTok + rl + 8 * i) >> A.lb;
-        const int v = b < nblk ? row[b] : -1;
-        id[i] = v < A.n_blocks ? v : -1;
+    int g_gone = 0, k = -1, j = 0, hi = 0, h = 0, nblk = 0;
+    const int* row = nullptr;
+    Next nxt;
+    const auto advance = [&](Next& N) {                    // one token tile on: false after the last
+      if (++j >= hi) {
+        do {
+          if (k >= 0) give_back(k);
+          if (!take(++k)) return false;
+          j = items[k % kItems].lo;
+          hi = items[k % kItems].hi;
+        } while (hi <= j);
+        const Item& I = items[k % kItems];
+        h = I.h;
+        nblk = blocks_of(I.L, A.lb);
+        row = A.table + (size_t)I.req * A.max_blocks;
       }
-    };
-    const auto load = [&](const uint8_t* codes, int j, uint4 (&x)[4 * H]) {
+      const int t = j * kTileTok + 32 * w;
+      N.h = h;
+      N.o = t & ((1 << A.lb) - 1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int o = (t_begin + j * kTileTok + rl + 8 * i) & ((1 << A.lb) - 1);
-        const uint4* at = reinterpret_cast<const uint4*>(codes + (id[i] < 0 ? 0 : id[i]) * blk_bytes + head_off + (size_t)o * D) + c;
-#pragma unroll
-        for (int q = 0; q < H; ++q) x[i * H + q] = id[i] >= 0 ? __ldg(at + 4 * q) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 2; ++i) {
+        const int b = (t + 16 * i) >> A.lb;
+        N.id[i] = b < nblk ? row[b] : -2;                  // -2: past the request's blocks
       }
+      return true;
     };
-    // scales of this warp's two groups of 16 tokens: lanes 0-15 and 16-31 hold the first's and the second's
-    const auto scales = [&]() {
-      const int b = lane < 16 ? id[0] : id[2];
+    // codes and scales of tile N (scales: lanes 0-15 and 16-31 hold the first group's and the second's)
+    const auto load = [&](Next N) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (N.id[i] == -1 || N.id[i] < -2 || N.id[i] >= A.n_blocks) {
+          record_status(SVDQ_ERR_INVALID_ARG);
+          N.id[i] = -1;
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int id = N.id[g], o = ((N.o + 16 * g) & ((1 << A.lb) - 1)) + r4;
+        const size_t at = ((((size_t)max(id, 0) * A.kv + N.h) << A.lb) + o) * D + 16 * c;
+        const uint4 *pk = reinterpret_cast<const uint4*>(A.kc + at), *pv = reinterpret_cast<const uint4*>(A.vc + at);
+#pragma unroll
+        for (int i = 2 * g; i < 2 * g + 2; ++i)
+#pragma unroll
+          for (int q = 0; q < H; ++q) {
+            kr[i * H + q] = id >= 0 ? ld_stream(pk + (i & 1) * (8 * D / 16) + 4 * q) : make_uint4(0, 0, 0, 0);
+            vr[i * H + q] = id >= 0 ? ld_stream(pv + (i & 1) * (8 * D / 16) + 4 * q) : make_uint4(0, 0, 0, 0);
+          }
+      }
+      const int b = lane < 16 ? N.id[0] : N.id[1];
       g_gone = b < 0;
-      g_sk = b < 0 ? 0.0f : A.ks[(size_t)b * A.kv + h];
-      g_sv = b < 0 ? 0.0f : A.vs[(size_t)b * A.kv + h];
+      g_sk = b < 0 ? 0.0f : A.ks[(size_t)b * A.kv + N.h];
+      g_sv = b < 0 ? 0.0f : A.vs[(size_t)b * A.kv + N.h];
     };
-    if (tiles > 0) {
-      ids(0);
-      load(A.kc, 0, kr);
-      load(A.vc, 0, vr);
-      scales();
+    bool more = advance(nxt), after = false;
+    if (more) {
+      load(nxt);
+      after = advance(nxt);
     }
-    for (int j = 0; j < tiles; ++j) {
-      const int st = j & 1;
-      if (j >= 2 && !mbar_wait(&k_empty[st], ((j >> 1) & 1) ^ 1, &s_abort)) break;
+    for (int t = 0; more; ++t) {
+      const int st = t & 1;
+      if (t >= 2 && !mbar_wait(&k_empty[st], ((t >> 1) & 1) ^ 1, &s_abort)) break;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int q = 0; q < H; ++q) store_codes<FMT>(sk + st * TB, rl + 8 * i, q, c, kr[i * H + q]);
-      if ((lane & 15) == 0) {
-        TileMeta* M = meta + (j & (kTileMeta - 1)) * 8 + 2 * w + (lane >> 4);
-        // a scale below 2^-60 of the largest counts as that: its values are lost beside it either way
-        const float ratio = vref > 0.0f ? fmaxf(__fdiv_rn(g_sv, vref), 0x1p-60f) : 1.0f;
-        *M = TileMeta{g_sk, log2f(ratio), __fdiv_rn(1.0f, ratio), g_gone};
-      }
+        for (int q = 0; q < H; ++q) store_codes<FMT>(sk + st * TB, 32 * w + r4 + 8 * i, q, c, kr[i * H + q]);
+      if ((lane & 15) == 0)
+        meta[(t & (kTileMeta - 1)) * 8 + 2 * w + (lane >> 4)] = TileMeta{g_sk, g_sv > 0.0f ? log2f(g_sv) : -INFINITY, g_gone, 0};
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&k_full[st]);
-      if (j + 1 < tiles) {
-        ids(j + 1);
-        load(A.kc, j + 1, kr);
-        scales();
-      }
-      if (j >= 2 && !mbar_wait(&v_empty[st], ((j >> 1) & 1) ^ 1, &s_abort)) break;
+      if (t >= 2 && !mbar_wait(&v_empty[st], ((t >> 1) & 1) ^ 1, &s_abort)) break;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int q = 0; q < H; ++q) store_codes<FMT>(sv + st * TB, rl + 8 * i, q, c, vr[i * H + q]);
+        for (int q = 0; q < H; ++q) store_codes<FMT>(sv + st * TB, 32 * w + r4 + 8 * i, q, c, vr[i * H + q]);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&v_full[st]);
-      if (j + 1 < tiles) load(A.vc, j + 1, vr);
+      // the next loads go out only here: the fences above wait for loads in flight
+      more = after;
+      if (more) {
+        load(nxt);
+        after = advance(nxt);
+      }
     }
   } else {
-    regs_dec<48>();
-    if (warp == 12 && lane == 0) {
-      constexpr uint32_t kIdS = idesc_f16_f16(128, 128), kIdO = idesc_f16_f16(128, D) | (1u << 16);
-      const auto issue_s = [&](int rt, int j) {
-        const uint32_t a = smem_u32(sq + rt * TB), b = smem_u32(sk + (j & 1) * TB);
+  regs_dec<96>();
+  if (warp == 12) {
+    constexpr uint32_t kIdS = idesc_f16_f16(128, 128), kIdO = idesc_f16_f16(128, D) | (1u << 16);
+    const uint64_t dq = desc_k_sw128(smem_u32(sq)), dk = desc_k_sw128(smem_u32(sk)), dv = desc_mn_sw128(smem_u32(sv));
+    const bool leader = elect_one();
+    // a token tile: its row tiles' tiles end at e0 and e1
+    struct Tile { int j, lo, hi, e0, e1; };
+    int k = 0;
+    const auto advance = [&](Tile& T) {
+      if (++T.j < T.hi) return true;
+      do {
+        if (!take(k)) return false;
+        const Item& I = items[k % kItems];
+        T = Tile{I.lo, I.lo, I.hi, I.end[0], I.end[1]};
+        give_back(k++);
+      } while (T.hi <= T.lo);
+      return true;
+    };
+    const auto issue_s = [&](int rt, int st) {
+      const uint64_t a = dq + rt * (TB >> 4), b = dk + st * (TB >> 4);
+      if (leader) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t o = (k >> 2) * kTileHalf + (k & 3) * 32;
-          mma_f16(tm + rt * 128, desc_k_sw128(a + o), desc_k_sw128(b + o), kIdS, k > 0);
+        for (int i = 0; i < D / 16; ++i) {
+          constexpr int kHalf = kTileHalf >> 4;
+          const int o = (i >> 2) * kHalf + (i & 3) * 2;
+          mma_f16(tm + rt * 128, a + o, b + o, kIdS, i > 0);
         }
         mma_commit(&s_full[rt]);
-      };
-      const auto issue_o = [&](int rt, int j) {
-        const uint32_t b = smem_u32(sv + (j & 1) * TB);
+      }
+    };
+    const auto issue_o = [&](int rt, int st, int half, bool fresh) {   // 64 tokens
+      const uint64_t b = dv + st * (TB >> 4);
+      if (leader) {
 #pragma unroll
-        for (int k = 0; k < kTileTok / 16; ++k)
-          mma_f16_ts(tm + 256 + rt * D, tm + rt * 128 + 8 * k, desc_mn_sw128(b + k * 2048), kIdO, j > 0 || k > 0);
-      };
-      bool ok = tiles == 0 || mbar_wait(&k_full[0], 0, &s_abort);
-      if (ok && tiles > 0) {
+        for (int i = 4 * half; i < 4 * half + 4; ++i)
+          mma_f16_ts(tm + 256 + rt * D, tm + rt * 128 + 8 * i, b + i * (2048 >> 4), kIdO, !fresh || i > 0);
+      }
+    };
+    const auto commit = [&](uint64_t* bar) { if (leader) mma_commit(bar); };
+    uint32_t n_p[2] = {0, 0}, n_q[2] = {0, 0};
+    bool ok = true;
+    // S of row tile rt at tile T (flat index t), where rt has one there
+    const auto next_s = [&](int rt, const Tile& T, int t) {
+      const int e = rt == 0 ? T.e0 : T.e1;
+      if (T.j >= e) return;
+      if (T.j == T.lo) {
+        ok = mbar_wait(&q_full[rt], n_q[rt] & 1, &s_abort);
+        ++n_q[rt];
+        if (!ok) return;
         tc_fence_after();
-        if (n0 > 0) issue_s(0, 0);
-        if (n1 > 0) issue_s(1, 0);
-        mma_commit(&k_empty[0]);
       }
-      for (int j = 0; ok && j < tiles; ++j) {
-        ok = mbar_wait(&v_full[j & 1], (j >> 1) & 1, &s_abort);
-        if (ok && j + 1 < tiles) ok = mbar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, &s_abort);
-        for (int rt = 0; ok && rt < 2; ++rt) {
-          const int n = rt == 0 ? n0 : n1;
-          if (j >= n) continue;
-          ok = mbar_wait(&p_full[rt], j & 1, &s_abort);
-          if (!ok) break;
-          tc_fence_after();
-          issue_o(rt, j);
-          if (j + 1 < n) issue_s(rt, j + 1);
-          else mma_commit(&o_full[rt]);
+      issue_s(rt, t & 1);
+    };
+    Tile cur = {0, 0, 0, 0, 0}, nxt;
+    bool more = advance(cur);
+    if (more) {
+      ok = mbar_wait(&k_full[0], 0, &s_abort);
+      tc_fence_after();
+      for (int rt = 0; ok && rt < 2; ++rt) next_s(rt, cur, 0);
+      commit(&k_empty[0]);
+    }
+    for (int t = 0; more && ok; ++t) {
+      nxt = cur;
+      more = advance(nxt);
+      ok = mbar_wait(&v_full[t & 1], (t >> 1) & 1, &s_abort);
+      if (ok && more) ok = mbar_wait(&k_full[(t + 1) & 1], ((t + 1) >> 1) & 1, &s_abort);
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) {
+        const int e = rt == 0 ? cur.e0 : cur.e1;
+        if (ok && cur.j < e) {
+          ok = mbar_wait(&p1_full[rt], n_p[rt] & 1, &s_abort);
+          if (ok) {
+            tc_fence_after();
+            issue_o(rt, t & 1, 0, cur.j == cur.lo);
+            commit(&o1_full[rt]);
+            ok = mbar_wait(&p_full[rt], n_p[rt] & 1, &s_abort);
+          }
+          ++n_p[rt];
+          if (ok) {
+            tc_fence_after();
+            issue_o(rt, t & 1, 1, false);
+            if (cur.j + 1 == e) commit(&o_full[rt]);
+          }
         }
-        if (!ok) break;
-        mma_commit(&v_empty[j & 1]);
-        if (j + 1 < tiles) mma_commit(&k_empty[(j + 1) & 1]);
+        if (ok && more) next_s(rt, nxt, t + 1);
       }
-      if (!ok) {                                         // gave up: the MMAs in flight end before TMEM is freed
-        int own = 0;
-        mma_commit(drained);
-        mbar_wait(drained, 0, &own);
+      if (!ok) break;
+      if (more) {
+        commit(&v_empty[t & 1]);
+        commit(&k_empty[(t + 1) & 1]);
       }
+      cur = nxt;
+    }
+    if (!ok) {                                             // gave up: the MMAs in flight end before TMEM is freed
+      int own = 0;
+      commit(drained);
+      mbar_wait(drained, 0, &own);
     }
     __syncwarp();
+  } else if (warp == 13) {
+    Walk walk;
+    if (lane < 2 && A.pieces) A.pieces[blockIdx.x * 2 + lane].valid = 0;
+    __syncwarp();
+    bool left = share.req >= 0;
+    if (left) walk.start(A, share, kTileRows);
+    for (int k = 0;; ++k) {
+      Item I;
+      left = left && walk.next(A, share, kTileRows, I);
+      if (!left) I.hi = -1;
+      if (k >= kItems && !mbar_wait(&i_empty[k % kItems], (k / kItems - 1) & 1, &s_abort)) break;
+      if (lane == 0) {
+        items[k % kItems] = I;
+        mbar_arrive(&i_full[k % kItems]);
+        if (left && I.out != kItemWhole) {
+          const Rows R = {I.a, I.n, I.L, I.rows};
+          const int tiles = (seen_by(A, R, min(I.rows, I.r0 + kTileRows) - 1) + kTileTok - 1) / kTileTok;
+          A.pieces[blockIdx.x * 2 + I.out] = Piece{1, I.hi == tiles, I.a, min(kTileRows, I.rows - I.r0), I.h, I.r0, 0, 0};
+        }
+      }
+      __syncwarp();
+      if (!left) break;
+    }
+  }
   }
   tc_fence_before();
   __syncthreads();
@@ -1248,17 +1578,94 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
   }
 }
 
+// Adds the pieces of the items that a border of the schedule cut: blockIdx.x is the
+// CTA whose last item continues in the CTAs after it, blockIdx.y a part of its rows,
+// a warp per row.  Pieces are added in the order of their tokens.
+constexpr int kJoinWarps = 8, kMaxParts = 1024;
+template <int DT, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnArgs A, int parts, int cr) {
+  constexpr int V = D / 32;                              // values a lane
+  __shared__ uint8_t s_state[kMaxParts];                 // bit 0: holds a piece, bit 1: the item's last
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x;
+  griddep_wait();
+  const Piece P = A.pieces[c0 * 2 + 1];
+  if (!P.valid) return;
+  for (int k = c0 + 1 + threadIdx.x; k < parts; k += kJoinWarps * 32)
+    s_state[k] = (uint8_t)(A.pieces[k * 2].valid | A.pieces[k * 2].last << 1);
+  __syncthreads();
+  for (int r = blockIdx.y * kJoinWarps + warp; r < P.n_rows; r += gridDim.y * kJoinWarps) {
+    float m = -INFINITY, l = 0.0f, v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.0f;
+    int k = c0, next = c0 + 1;
+    while (k >= 0) {
+      // four pieces at a time: loads first
+      size_t cell[4];
+      int n = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (k >= 0) {
+          cell[b] = ((size_t)k * 2 + (k == c0)) * cr + r;
+          n = b + 1;
+          const bool end = k != c0 && (s_state[k] & 2);
+          while (!end && next < parts && !(s_state[next] & 1)) ++next;
+          k = end || next >= parts ? -1 : next++;
+        }
+      }
+      float2 ml[4];
+      float x[4][V], top = m;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        ml[b] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[b][i] = 0.0f;
+        if (b < n) {
+          ml[b] = *reinterpret_cast<const float2*>(A.part_ml + cell[b] * 2);
+          const float* src = A.part_o + cell[b] * D + V * lane;
+          if constexpr (V == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(src);
+            x[b][0] = y.x; x[b][1] = y.y; x[b][2] = y.z; x[b][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(src);
+            x[b][0] = y.x; x[b][1] = y.y;
+          }
+        }
+        top = fmaxf(top, ml[b].x);
+      }
+      const float back = m == -INFINITY ? 0.0f : ex2(m - top);
+      m = top;
+      l *= back;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= back;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float w = ml[b].x == -INFINITY ? 0.0f : ex2(ml[b].x - m);
+        l += w * ml[b].y;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += w * x[b][i];
+      }
+    }
+    const int row = P.r0 + r;
+    const float mul = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+    uint16_t* dst = A.out + (int64_t)(P.token + row / A.G) * A.out_stride + (int64_t)(P.h * A.G + row % A.G) * D + V * lane;
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) w[i] = (uint32_t)store16<DT>(v[2 * i] * mul) | ((uint32_t)store16<DT>(v[2 * i + 1] * mul) << 16);
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = w[0];
+  }
+}
+
 // Joins the splits of a row in a fixed order: a CTA per row, warp w takes splits w,
 // w + 4, ..., then the warps in order.  Rows whose tokens fitted one split were
 // written already.
-constexpr int kJoinWarps = 4;
 template <int DT, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnArgs A, int tile_rows) {
+__global__ void __launch_bounds__(128) paged_join_splits_kernel(const AttnArgs A, int tile_rows) {
   constexpr int V = D / 32;                              // values a lane
-  __shared__ float s_v[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
+  __shared__ float s_v[4][D], s_m[4], s_l[4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.x, h = blockIdx.y, req = blockIdx.z;
   griddep_wait();
-  const Rows R = request_rows(A, req);
+  const Rows R = request_rows(A, req, threadIdx.x == 0);
   if (r >= R.rows) return;
   const int vis = seen_by(A, R, min(R.rows, (r / tile_rows + 1) * tile_rows) - 1);
   if (vis <= A.chunk) return;
@@ -1268,12 +1675,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnA
   float m = -INFINITY, l = 0.0f, v[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) v[k] = 0.0f;
-  for (int s0 = warp; s0 < n; s0 += 8 * kJoinWarps) {
+  for (int s0 = warp; s0 < n; s0 += 8 * 4) {
     float2 ml[8];
     float x[8][V], top = m;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int s = s0 + i * kJoinWarps;
+      const int s = s0 + i * 4;
       const size_t c = cell + (size_t)s * step;
       ml[i] = s < n ? *reinterpret_cast<const float2*>(A.part_ml + c * 2) : make_float2(-INFINITY, 0.0f);
 #pragma unroll
@@ -1301,9 +1708,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnA
   if (threadIdx.x >= D) return;
   float M = -INFINITY, L = 0.0f, y = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_m[w]);
+  for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w]);
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
+  for (int w = 0; w < 4; ++w) {
     const float b = s_m[w] == -INFINITY ? 0.0f : ex2(s_m[w] - M);
     L += b * s_l[w];
     y += b * s_v[w][threadIdx.x];
@@ -1326,7 +1733,7 @@ int log2_block(int bs) {
 
 svdq_status check_cache(const svdq_paged_cache* c) {
   if (!c || c->reserved != 0) return SVDQ_ERR_INVALID_ARG;
-  if (c->heads < 1 || c->kv_heads < 1 || c->heads % c->kv_heads != 0 || c->n_blocks < 1 || c->heads > 65535)
+  if (c->heads < 1 || c->kv_heads < 1 || c->heads % c->kv_heads != 0 || c->n_blocks < 1 || c->heads > 32768)
     return SVDQ_ERR_INVALID_ARG;
   if ((c->fmt != SVDQ_KV_INT8 && c->fmt != SVDQ_KV_E4M3) || (c->dtype != SVDQ_BF16 && c->dtype != SVDQ_F16))
     return SVDQ_ERR_INVALID_ARG;
@@ -1407,6 +1814,7 @@ svdq_status launched(const char* where) {
 // The SM count that the split aims at: fixed, so that workspace sizes can be asked
 // for without a device.
 constexpr int kSplitSms = 148;
+constexpr int kMinTiles = 1;
 
 // How a call's rows and tokens are split: CTAs of `cta_rows` rows (8, 16: the few-row
 // kernel; 128, 256: the tensor-core kernel) x `splits` ranges of tokens.  Up to
@@ -1429,19 +1837,35 @@ Split split_of(const svdq_paged_cache* c, const svdq_paged_batch* b, int sms) {
     if (!s.cluster) s.splits = (int)((len + s.chunk - 1) / s.chunk);
     return s;
   }
-  s.cta_rows = rows > 128 && ctas(256) >= sms ? 256 : 128;
-  s.row_ctas = (int)((rows + s.cta_rows - 1) / s.cta_rows);
-  s.cluster = 0;
-  const int64_t n = ctas(s.cta_rows), want = std::max<int64_t>(1, std::min((sms + n - 1) / n, (len + 1023) / 1024));
-  s.chunk = (int)(((len + want - 1) / want + kTileTok - 1) / kTileTok * kTileTok);
-  s.splits = (int)((len + s.chunk - 1) / s.chunk);
+  // one CTA per SM, fewer where that leaves one less than kMinTiles token tiles
+  const int64_t items = std::min(ctas(kTileRows), ((int64_t)b->n_tokens * (c->heads / c->kv_heads) / kTileRows + b->B) * c->kv_heads);
+  const int64_t tiles = items * ((len + kTileTok - 1) / kTileTok);
+  s = Split{kTileRows, 0, (int)std::clamp<int64_t>(tiles / kMinTiles, 1, sms), 0, 0};
   return s;
 }
 
 size_t attention_ws(const svdq_paged_cache* c, const svdq_paged_batch* b) {
   const Split s = split_of(c, b, kSplitSms);
   if (s.splits <= 1 || s.cluster) return 16;
+  if (s.cta_rows == kTileRows) return (size_t)s.splits * 2 * (sizeof(Piece) + kTileRows * (size_t)(c->head_dim + 2) * sizeof(float));
   return (size_t)s.splits * b->n_tokens * c->heads * (size_t)(c->head_dim + 2) * sizeof(float);
+}
+
+// A launch that may start while the kernel before it on the stream still runs (each
+// kernel waits for that one before it touches memory).
+template <class... P, class... Q>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, const Q&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int DT, int FMT, int D, int NB>
@@ -1468,24 +1892,15 @@ svdq_status launch_attention(const AttnArgs& A, const Split& s, cudaStream_t str
     e = s.cta_rows == 8 ? launch_rows<DT, FMT, D, 1>(A, s, stream) : launch_rows<DT, FMT, D, 2>(A, s, stream);
     if (e != cudaSuccess) return cuda_failure(e, "paged_rows_kernel launch");
   } else {
-    const int64_t grid = (int64_t)s.splits * s.row_ctas * A.B * A.kv;
-    if (grid > INT32_MAX) return SVDQ_ERR_UNSUPPORTED;
-    paged_tiles_kernel<DT, FMT, D><<<(unsigned)grid, kTileThreads, tiles_smem(D), stream>>>(A, s.cta_rows);
-    const svdq_status st = launched("paged_tiles_kernel launch");
-    if (st != SVDQ_OK) return st;
+    e = launch_after(paged_tiles_kernel<DT, FMT, D>, dim3((unsigned)s.splits), kTileThreads, tiles_smem(D), stream, A);
+    if (e != cudaSuccess) return cuda_failure(e, "paged_tiles_kernel launch");
+    if (s.splits <= 1) return SVDQ_OK;
+    e = launch_after(paged_join_kernel<DT, D>, dim3((unsigned)s.splits, 8u), kJoinWarps * 32, 0, stream, A, s.splits, kTileRows);
+    return e == cudaSuccess ? SVDQ_OK : cuda_failure(e, "paged_join_kernel launch");
   }
   if (s.splits <= 1 || s.cluster) return SVDQ_OK;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(A.max_new * A.G), (unsigned)A.kv, (unsigned)A.B);
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_join_kernel<DT, D>, A, s.cta_rows);
-  return e == cudaSuccess ? SVDQ_OK : cuda_failure(e, "paged_join_kernel launch");
+  e = launch_after(paged_join_splits_kernel<DT, D>, dim3((unsigned)(A.max_new * A.G), (unsigned)A.kv, (unsigned)A.B), 128, 0, stream, A, s.cta_rows);
+  return e == cudaSuccess ? SVDQ_OK : cuda_failure(e, "paged_join_splits_kernel launch");
 }
 
 template <int DT, int FMT, int D>
@@ -1624,11 +2039,19 @@ svdq_status svdq_paged_attention(const svdq_paged_cache* c, const svdq_paged_bat
   A.table = b->table; A.lens = b->lens; A.cu = b->cu;
   A.part_o = static_cast<float*>(workspace);
   A.part_ml = A.part_o + (size_t)sp.splits * b->n_tokens * c->heads * c->head_dim;
+  A.pieces = nullptr;
+  if (sp.cta_rows == kTileRows && sp.splits > 1) {
+    A.pieces = static_cast<Piece*>(workspace);
+    A.part_ml = reinterpret_cast<float*>(A.pieces + sp.splits * 2);
+    A.part_o = A.part_ml + (size_t)sp.splits * 2 * kTileRows * 2;
+  }
   A.q_stride = q_stride; A.out_stride = out_stride;
   A.B = b->B; A.max_blocks = b->max_blocks; A.n_tokens = b->n_tokens; A.max_new = b->max_new; A.max_len = b->max_len;
   A.n_blocks = c->n_blocks; A.heads = c->heads; A.kv = c->kv_heads; A.G = c->heads / c->kv_heads;
   A.lb = log2_block(c->block_size); A.causal = causal; A.splits = sp.splits; A.chunk = sp.chunk;
   A.scale_log2 = scale * 1.4426950408889634f;
+  A.inv_parts = 1.0 / sp.splits;
+  A.g_inv = A.G == 1 ? 0u : (uint32_t)(((1ull << 32) + A.G - 1) / A.G);
   return by_types(c, AttnCall{A, sp, reinterpret_cast<cudaStream_t>(stream)});
 }
 
