@@ -77,6 +77,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
   __shared__ int w_take[kPlanThreads / 32], w_give[kPlanThreads / 32], s_bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) s_bad = 0;
+  griddep_wait();
+  griddep_launch();
   __syncthreads();
   const int head = A.state_in[0], count = A.state_in[1];
   long long c_new = 0;
@@ -174,8 +176,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
 // block: bs d values) are read once and stay in registers between the maximum
 // and the codes.  Work index w -> request: request i owns the indices from
 // floor(cu_i / bs) + 2 i, which leaves it at least as many as it touches blocks
-// (<= floor(new / bs) + 2), so the grid needs only n_tokens and B on the host.
-constexpr int kAppendThreads = 128;
+// (<= floor(new / bs) + 2), so the grid needs only n_tokens and B on the host; + i
+// where no request has more than one new token.
+constexpr int append_threads(int BS, int D) { return BS * D >= 16384 ? 256 : 128; }
 
 template <int FMT> struct Fmt;
 template <> struct Fmt<SVDQ_KV_INT8> { static constexpr float qmax = 127.0f; };
@@ -199,12 +202,13 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
 
 // x / s as IEEE division rounds it: q = RN(x rs) is within an ulp, e = x - q s is
 // exact (one FMA), RN(q + e rs) is the correctly rounded quotient (Markstein) while
-// nothing under- or overflows; rs = 0 outside 2^-60 <= s <= 2^60 (division then).
+// nothing under- or overflows: for 2^-60 <= s <= 2^60, rs = RN(1 / s).
 __device__ __forceinline__ float quotient(float x, float s, float rs) {
-  if (rs == 0.0f) return s > 0.0f ? __fdiv_rn(x, s) : 0.0f;
   const float q = __fmul_rn(x, rs);
   return __fmaf_rn(__fmaf_rn(-q, s, x), rs, q);
 }
+
+__device__ __noinline__ float divide_rn(float x, float s) { return __fdiv_rn(x, s); }
 
 // Four values to four codes, round to nearest even, saturating.
 template <int FMT>
@@ -238,25 +242,29 @@ struct AppendArgs {
   float* scale[2];
   const int* cu;
   const int* slots;
-  int B, n_tokens, kv, n_blocks;
+  int B, n_tokens, kv, n_blocks, max_new, per;   // per: spare work indices a request
 };
 
 template <int DT, int FMT, int D, int LB>
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs A) {
+__global__ void __launch_bounds__(append_threads(1 << LB, D)) paged_append_kernel(const AppendArgs A) {
+  constexpr int kAppendThreads = append_threads(1 << LB, D);
   constexpr int BS = 1 << LB, kPerRow = D / 8, kRows = kAppendThreads / kPerRow, kPass = BS / kRows > 0 ? BS / kRows : 1;
   __shared__ float s_amax[kAppendThreads / 32];
   const int tid = threadIdx.x, w = blockIdx.x, h = blockIdx.y, which = blockIdx.z;
+  griddep_wait();
+  griddep_launch();
   // this work item's request: the last one whose first index is not above w
   int i = -1;
   for (int r0 = 0; r0 < A.B; r0 += kAppendThreads) {
     const int r = r0 + tid;
-    const bool le = r < A.B && (clampi(A.cu[r], 0, A.n_tokens) >> LB) + 2 * r <= w;
+    const bool le = r < A.B && (clampi(A.cu[r], 0, A.n_tokens) >> LB) + A.per * r <= w;
     i += __syncthreads_count(le);
   }
   if (i < 0) return;
   const int a = clampi(A.cu[i], 0, A.n_tokens), e = clampi(A.cu[i + 1], 0, A.n_tokens);
   if (a >= e) return;
-  const int j = w - (a >> LB) - 2 * i, o0 = A.slots[a] & (BS - 1);
+  if (e - a > A.max_new && tid == 0) record_status(SVDQ_ERR_INVALID_ARG);
+  const int j = w - (a >> LB) - A.per * i, o0 = A.slots[a] & (BS - 1);
   const int64_t first = (int64_t)a + (j == 0 ? 0 : (int64_t)j * BS - o0);
   if (first >= e) return;
   const int t0 = (int)first;
@@ -269,9 +277,12 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
   }
   const int rows = min(min(e, a + (j + 1) * BS - o0) - t0, BS - off);
   const int c = tid % kPerRow, r0 = tid / kPerRow;
-  const uint16_t* x = A.x[which] + (int64_t)t0 * A.stride[which] + h * D + 8 * c;
+  // chosen, not indexed: an index into the arguments would copy them to local memory
+  const int64_t stride = which ? A.stride[1] : A.stride[0];
+  const uint16_t* x = (which ? A.x[1] : A.x[0]) + (int64_t)t0 * stride + h * D + 8 * c;
+  float* scale = which ? A.scale[1] : A.scale[0];
   const size_t cell = (size_t)blk * A.kv + h;
-  const float s_old = off > 0 ? A.scale[which][cell] : 0.0f;
+  const float s_old = off > 0 ? scale[cell] : 0.0f;
   uint4 v[kPass];
   int at[kPass];
   uint32_t have = 0;
@@ -283,7 +294,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
     v[p] = make_uint4(0, 0, 0, 0);
     at[p] = -1;
     if (r < rows) {
-      v[p] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)r * A.stride[which]));
+      v[p] = *reinterpret_cast<const uint4*>(x + (int64_t)r * stride);
       at[p] = A.slots[t0 + r];
     }
   }
@@ -307,9 +318,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
 #pragma unroll
   for (int k = 0; k < kAppendThreads / 32; ++k) amax = fmaxf(amax, s_amax[k]);
   const float s = fmaxf(s_old, __fdiv_rn(amax, Fmt<FMT>::qmax));
-  uint8_t* base = A.codes[which] + cell * (size_t)(BS * D);
+  uint8_t* base = (which ? A.codes[1] : A.codes[0]) + cell * (size_t)(BS * D);
   if (s > s_old) {
-    if (tid == 0) A.scale[which][cell] = s;
+    if (tid == 0) scale[cell] = s;
     const float ratio = __fdiv_rn(s_old, s);
     for (int p = tid; p < off * D / 16; p += kAppendThreads) {
       uint4* at = reinterpret_cast<uint4*>(base) + p;
@@ -325,19 +336,30 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
       *at = q;
     }
   } else if (off == 0 && tid == 0) {
-    A.scale[which][cell] = 0.0f;                     // a fresh block of zeros
+    scale[cell] = 0.0f;                     // a fresh block of zeros
   }
-  const float rs = s >= 0x1p-60f && s <= 0x1p+60f ? __frcp_rn(s) : 0.0f;
+  // two copies of the loop: with the division inlined at every value the code left the
+  // instruction cache (47 us where the fast copy alone takes FASTUS on 15,000 tokens)
+  const auto write = [&](auto divide) {
 #pragma unroll
-  for (int p = 0; p < kPass; ++p) {
-    if (have >> p & 1u) {
-      float f[8];
-      unpack8<DT>(v[p], f);
+    for (int p = 0; p < kPass; ++p) {
+      if (have >> p & 1u) {
+        float f[8];
+        unpack8<DT>(v[p], f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = quotient(f[k], s, rs);
-      *reinterpret_cast<uint2*>(base + (size_t)(off + r0 + p * kRows) * D + 8 * c) =
-          make_uint2(codes4<FMT>(f[0], f[1], f[2], f[3]), codes4<FMT>(f[4], f[5], f[6], f[7]));
+        for (int k = 0; k < 8; ++k) f[k] = divide(f[k]);
+        *reinterpret_cast<uint2*>(base + (size_t)(off + r0 + p * kRows) * D + 8 * c) =
+            make_uint2(codes4<FMT>(f[0], f[1], f[2], f[3]), codes4<FMT>(f[4], f[5], f[6], f[7]));
+      }
     }
+  };
+  if (s >= 0x1p-60f && s <= 0x1p+60f) {
+    const float rs = __frcp_rn(s);
+    write([&](float x) { return quotient(x, s, rs); });
+  } else if (s > 0.0f) {
+    write([&](float x) { return divide_rn(x, s); });
+  } else {
+    write([](float) { return 0.0f; });
   }
 }
 
@@ -360,13 +382,14 @@ struct AttnArgs {
   const int* table;
   const int* lens;
   const int* cu;
-  float* part_o;           // [splits][n_tokens][heads][d]; many rows: [CTA][2][256][d]
-  float* part_ml;          // [splits][n_tokens][heads][2]; many rows: [CTA][2][256][2]
-  struct Piece* pieces;    // many rows: [CTA][2]
+  float* part_o;           // pieces of cut items: [CTA][2][rows][d]
+  float* part_ml;          // [CTA][2][rows][2]
+  struct Piece* pieces;    // [CTA][2]
   int64_t q_stride, out_stride;
-  int B, max_blocks, n_tokens, max_new, max_len, n_blocks, heads, kv, G, lb, causal, splits, chunk;
+  int B, max_blocks, n_tokens, max_new, max_len, n_blocks, heads, kv, G, lb, causal, splits;
   float scale_log2;
   double inv_parts;        // 1 / CTAs of the schedule
+  int snap;                // items are not cut
   uint32_t g_inv;          // ceil(2^32 / G), 0 for G = 1: x / G is exact for x G < 2^32
 };
 
@@ -431,6 +454,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+constexpr float kGrow = 7.0f, kGrowFactor = 128.0f;   // a softmax reference may lag by this much (2^7)
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -455,10 +480,11 @@ __device__ __forceinline__ void load_queries(const AttnArgs& A, const Rows& R, i
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const int e = clampi((int)(__float_as_uint(top) >> 23) - 127, -100, 100);
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+    // the factor is kept non-negative (maxima are taken before it): a negative scale turns the query instead
+    const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), A.scale_log2);
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) sq[rr * (D + 8) + lane + 32 * k] = __float2half_rn(v[k] * down);
-    if (lane == 0) sf[rr] = __uint_as_float((uint32_t)(127 + e) << 23) * A.scale_log2;
+    if (lane == 0) sf[rr] = __uint_as_float((uint32_t)(127 + e) << 23) * fabsf(A.scale_log2);
   }
 }
 
@@ -468,8 +494,9 @@ __device__ __forceinline__ void load_queries(const AttnArgs& A, const Rows& R, i
 // the MMAs and accumulators of the other way round).  Each of the 4 warps takes every
 // fourth tile of 32 tokens through a ring of its own (bulk copies, no barrier between
 // warps) and keeps its own m, l and accumulator; the warps' results are joined at the
-// end, then those of the CTAs of a cluster, which share the tokens of a (request, kv
-// head) evenly.  The fragments are read straight from the codes: the order of the
+// end.  Few (request, kv head) cells: a cluster of CTAs shares a cell's tokens evenly and
+// joins in shared memory (paged_rows_kernel).  Many cells, or long ones: the balanced
+// schedule (paged_flat_kernel).  The fragments are read straight from the codes: the order of the
 // contraction over d is free, so 16 bytes of a key row serve 4 k-steps, and 16 bytes
 // of four value rows the 16 values of d that a lane needs.
 constexpr int kDecWarps = 4, kDecTile = 32, kDecStages = 2, kDecGroup = 16, kMaxCluster = 8;
@@ -500,9 +527,203 @@ __device__ __forceinline__ void store_row4(uint16_t* dst, const float4& v, float
   *reinterpret_cast<uint2*>(dst) = w;
 }
 
+// The same pair as half2_of, E4M3 by the conversion instruction: its value, NaN codes NaN.
+template <int FMT, int HI>
+__device__ __forceinline__ uint32_t value2_of(uint32_t w) {
+  if constexpr (FMT == SVDQ_KV_INT8) {
+    return half2_of<FMT, HI>(w);
+  } else {
+    uint32_t y;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"((uint16_t)(HI ? w >> 16 : w & 0xFFFFu)));
+    return y;
+  }
+}
+
+// One warp's rows against its tokens: the query fragments, maxima, sums, accumulators.
+template <int FMT, int D, int NB>
+struct RowState {
+  static constexpr int KC = D / 64, VW = D / 32;
+  uint32_t qf[NB][D / 16][2];
+  float f[NB][2], o[D / 16][NB][4], m[NB][2], l[NB][2], vref, rv;   // rv = 1 / vref
+  int see[NB][2], clear, last;                                   // clear: tiles that end at or below it need no mask
+
+  // Q^T fragments: k-step s covers d = 64 (s / 4) + 16 q4 + 4 (s % 4) + {0, 1 | 2, 3}
+  __device__ __forceinline__ void start(const AttnArgs& A, const Rows& R, const __half* sq, const float* sf, int t_end, int lane) {
+    const int g = lane >> 2, q4 = lane & 3;
+    vref = rv = 0.0f;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        const uint2 w = *reinterpret_cast<const uint2*>(sq + (nb * 8 + g) * (D + 8) + (s >> 2) * 64 + q4 * 16 + 4 * (s & 3));
+        qf[nb][s][0] = w.x;
+        qf[nb][s][1] = w.y;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = nb * 8 + 2 * q4 + i;
+        f[nb][i] = sf[r];
+        see[nb][i] = r < R.rows ? min(t_end, seen_by(A, R, r)) : t_end;
+        m[nb][i] = -INFINITY;
+        l[nb][i] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) o[j][nb][0] = o[j][nb][1] = o[j][nb][2] = o[j][nb][3] = 0.0f;
+    }
+    clear = min(t_end, seen_by(A, R, 0));
+    last = t_end;
+  }
+
+  // 32 tokens from t on
+  __device__ __forceinline__ void step(const uint8_t* kt, const uint8_t* vt, const DecMeta& md, const int2& id, int t, int lane) {
+    const int g = lane >> 2, q4 = lane & 3;
+  // x[mt][nb]: tokens 16 mt + g (0, 1) and + 8 (2, 3), rows 8 nb + 2 q4 + {0, 1}
+    float x[2][NB][4];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) x[mt][nb][0] = x[mt][nb][1] = x[mt][nb][2] = x[mt][nb][3] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        const uint4 lo = *reinterpret_cast<const uint4*>(kt + (mt * 16 + g) * D + c * 64 + q4 * 16);
+        const uint4 hi = *reinterpret_cast<const uint4*>(kt + (mt * 16 + g + 8) * D + c * 64 + q4 * 16);
+        const uint32_t u[4] = {lo.x, lo.y, lo.z, lo.w}, w[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t y = pre<FMT>(u[i]), z = pre<FMT>(w[i]);
+          const uint32_t a[4] = {value2_of<FMT, 0>(y), value2_of<FMT, 0>(z), value2_of<FMT, 1>(y), value2_of<FMT, 1>(z)};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma16816(x[mt][nb], a, qf[nb][c * 4 + i][0], qf[nb][c * 4 + i][1]);
+        }
+      }
+    }
+    if (t + kDecTile > clear || id.x < 0 || id.y < 0) {
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const bool gone = (mt == 0 ? id.x : id.y) < 0;
+        const int tt = t + mt * 16 + g;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          if (gone || tt >= see[nb][0]) x[mt][nb][0] = -INFINITY;
+          if (gone || tt >= see[nb][1]) x[mt][nb][1] = -INFINITY;
+          if (gone || tt + 8 >= see[nb][0]) x[mt][nb][2] = -INFINITY;
+          if (gone || tt + 8 >= see[nb][1]) x[mt][nb][3] = -INFINITY;
+        }
+      }
+    }
+    // factors to units of log2 (-inf stays -inf in a block of zeros); a new reference only where a lane's
+    // scores, or the value scale, grew by 2^kGrow: no exchange between lanes otherwise
+    float fac[2][NB][2], top[NB][2];
+    bool grow = false;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        fac[0][nb][i] = fmaxf(f[nb][i] * md.sk[0], FLT_MIN);
+        fac[1][nb][i] = fmaxf(f[nb][i] * md.sk[1], FLT_MIN);
+        top[nb][i] = fmaxf(fmaxf(x[0][nb][i], x[0][nb][i + 2]) * fac[0][nb][i], fmaxf(x[1][nb][i], x[1][nb][i + 2]) * fac[1][nb][i]);
+        grow = grow || top[nb][i] > m[nb][i] + kGrow;
+      }
+    const float vmax = fmaxf(md.sv[0], md.sv[1]);
+    if (__any_sync(0xffffffffu, grow || vmax > vref * kGrowFactor)) {
+      float fv = 1.0f;
+      if (vmax > vref * kGrowFactor) {
+        fv = __fdiv_rn(vref, vmax);
+        vref = vmax;
+        rv = __fdiv_rn(1.0f, vref);
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float b[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) top[nb][i] = fmaxf(top[nb][i], __shfl_xor_sync(0xffffffffu, top[nb][i], s));
+          b[i] = 1.0f;
+          if (top[nb][i] > m[nb][i] + kGrow) {
+            b[i] = ex2(m[nb][i] - top[nb][i]);
+            l[nb][i] *= b[i];
+            m[nb][i] = top[nb][i];
+          }
+          b[i] *= fv;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          o[j][nb][0] *= b[0]; o[j][nb][1] *= b[1]; o[j][nb][2] *= b[0]; o[j][nb][3] *= b[1];
+        }
+      }
+    }
+    uint32_t pb[2][NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const float z0 = m[nb][0] == -INFINITY ? 0.0f : m[nb][0], z1 = m[nb][1] == -INFINITY ? 0.0f : m[nb][1];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const float wv = md.sv[mt] * rv;
+        const float p0 = ex2(fmaf(x[mt][nb][0], fac[mt][nb][0], -z0)), p1 = ex2(fmaf(x[mt][nb][1], fac[mt][nb][1], -z1));
+        const float p2 = ex2(fmaf(x[mt][nb][2], fac[mt][nb][0], -z0)), p3 = ex2(fmaf(x[mt][nb][3], fac[mt][nb][1], -z1));
+        l[nb][0] += p0 + p2;
+        l[nb][1] += p1 + p3;
+        // [token][row] -> [row][token]: the column operand of the second product
+        pb[mt][nb][0] = transpose8x8(pack_half2(p0 * wv, p1 * wv));
+        pb[mt][nb][1] = transpose8x8(pack_half2(p2 * wv, p3 * wv));
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint32_t u[4][VW];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint8_t* row = vt + (s * 16 + 2 * q4 + (r & 1) + (r >> 1) * 8) * D + g * (D / 8);
+        if constexpr (D == 128) {
+          const uint4 w = *reinterpret_cast<const uint4*>(row);
+          u[r][0] = pre<FMT>(w.x); u[r][1] = pre<FMT>(w.y); u[r][2] = pre<FMT>(w.z); u[r][3] = pre<FMT>(w.w);
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(row);
+          u[r][0] = pre<FMT>(w.x); u[r][1] = pre<FMT>(w.y);
+        }
+      }
+      const int there = (s == 0 ? id.x : id.y) < 0 ? 0 : last;
+      if (FMT == SVDQ_KV_E4M3 && t + s * 16 + 16 > there) {   // what no token wrote may be NaN codes
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (t + s * 16 + 2 * q4 + (r & 1) + (r >> 1) * 8 >= there) {
+#pragma unroll
+            for (int w = 0; w < VW; ++w) u[r][w] = 0;
+          }
+      }
+      // accumulator tile j: operand row n is d = (D / 8) n + 2 j, row n + 8 the d after it
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        const uint32_t la = __byte_perm(u[0][w], u[1][w], 0x5140), ha = __byte_perm(u[0][w], u[1][w], 0x7362);
+        const uint32_t lb = __byte_perm(u[2][w], u[3][w], 0x5140), hb = __byte_perm(u[2][w], u[3][w], 0x7362);
+        const uint32_t a0[4] = {value2_of<FMT, 0>(la), value2_of<FMT, 1>(la), value2_of<FMT, 0>(lb), value2_of<FMT, 1>(lb)};
+        const uint32_t a1[4] = {value2_of<FMT, 0>(ha), value2_of<FMT, 1>(ha), value2_of<FMT, 0>(hb), value2_of<FMT, 1>(hb)};
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          mma16816(o[2 * w][nb], a0, pb[s][nb][0], pb[s][nb][1]);
+          mma16816(o[2 * w + 1][nb], a1, pb[s][nb][0], pb[s][nb][1]);
+        }
+      }
+    }
+  }
+
+  // Sums over the warp's lanes; maxima and sums to wml (this warp's NR entries).
+  __device__ __forceinline__ void publish(float2* wml, int lane) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], s);
+        if (lane < 4) wml[nb * 8 + 2 * lane + i] = make_float2(m[nb][i], l[nb][i]);
+      }
+  }
+};
+
 template <int DT, int FMT, int D, int NB>
-__global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnArgs A, int cluster) {
-  constexpr int NST = kDecStages, kStage = dec_stage_bytes(D), KC = D / 64, VW = D / 32, NR = 8 * NB;
+__global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnArgs A) {
+  constexpr int NST = kDecStages, kStage = dec_stage_bytes(D), NR = 8 * NB;
   extern __shared__ __align__(128) uint8_t dsm[];
   uint8_t* ring = dsm;
   __half* sq = reinterpret_cast<__half*>(dsm + dec_ring_bytes(D));
@@ -515,14 +736,13 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
   __shared__ float s_vref[kDecWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
   const int h = blockIdx.y, req = blockIdx.z, split = blockIdx.x;
-  if (!cluster) griddep_launch();
-  const Rows R = request_rows(A, req, threadIdx.x == 0);
+  griddep_wait();
+  griddep_launch();
+  const Rows R = request_rows(A, req, tid == 0);
   if (R.rows == 0) return;
-  const int vis = seen_by(A, R, R.rows - 1), first_vis = seen_by(A, R, 0);
-  // a cluster shares what the rows see; otherwise a fixed chunk a split
-  const int chunk = cluster ? ((vis + A.splits - 1) / A.splits + kDecTile - 1) / kDecTile * kDecTile : A.chunk;
+  // the cluster shares what the rows see
+  const int vis = seen_by(A, R, R.rows - 1), chunk = ((vis + A.splits - 1) / A.splits + kDecTile - 1) / kDecTile * kDecTile;
   const int t_begin = split * chunk, t_end = max(t_begin, min(vis, t_begin + chunk));
-  if (!cluster && split > 0 && t_begin >= vis) return;
   if (tid == 0) {
     s_abort = 0;
     for (int s = 0; s < kDecWarps * NST; ++s) mbar_init(&bars[s], 1);
@@ -592,34 +812,8 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
 
   load_queries<DT, D>(A, R, h, 0, NR, sq, sf, warp, kDecWarps, lane);
   __syncthreads();
-  // Q^T fragments: k-step s covers d = 64 (s / 4) + 16 q4 + 4 (s % 4) + {0, 1 | 2, 3}
-  uint32_t qf[NB][D / 16][2];
-  float f[NB][2];
-  int see[NB][2];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      const uint2 w = *reinterpret_cast<const uint2*>(sq + (nb * 8 + g) * (D + 8) + (s >> 2) * 64 + q4 * 16 + 4 * (s & 3));
-      qf[nb][s][0] = w.x;
-      qf[nb][s][1] = w.y;
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = nb * 8 + 2 * q4 + i;
-      f[nb][i] = sf[r] * kUnit<FMT>;
-      see[nb][i] = r < R.rows ? min(t_end, seen_by(A, R, r)) : t_end;
-    }
-  }
-  const int clear = min(t_end, first_vis);              // tiles that end at or below this need no mask
-  float o[D / 16][NB][4], m[NB][2], l[NB][2], vref = 0.0f;
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    m[nb][0] = m[nb][1] = -INFINITY;
-    l[nb][0] = l[nb][1] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) o[j][nb][0] = o[j][nb][1] = o[j][nb][2] = o[j][nb][3] = 0.0f;
-  }
+  RowState<FMT, D, NB> S;
+  S.start(A, R, sq, sf, t_end, lane);
 
   for (int k = 0; k < mine; ++k) {
     const int st = k % NST, t = t_begin + (warp + kDecWarps * k) * kDecTile;
@@ -630,140 +824,13 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
     }
     const uint8_t* kt = wring + st * kStage;
     const uint8_t* vt = kt + kDecTile * D;
-    const DecMeta md = wmeta[k & (2 * kDecGroup - 1)];
-    const int2 id = wids[k & (2 * kDecGroup - 1)];
-    // x[mt][nb]: tokens 16 mt + g (0, 1) and + 8 (2, 3), rows 8 nb + 2 q4 + {0, 1}
-    float x[2][NB][4];
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) x[mt][nb][0] = x[mt][nb][1] = x[mt][nb][2] = x[mt][nb][3] = 0.0f;
-#pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const uint4 lo = *reinterpret_cast<const uint4*>(kt + (mt * 16 + g) * D + c * 64 + q4 * 16);
-        const uint4 hi = *reinterpret_cast<const uint4*>(kt + (mt * 16 + g + 8) * D + c * 64 + q4 * 16);
-        const uint32_t u[4] = {lo.x, lo.y, lo.z, lo.w}, w[4] = {hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t y = pre<FMT>(u[i]), z = pre<FMT>(w[i]);
-          const uint32_t a[4] = {half2_of<FMT, 0>(y), half2_of<FMT, 0>(z), half2_of<FMT, 1>(y), half2_of<FMT, 1>(z)};
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma16816(x[mt][nb], a, qf[nb][c * 4 + i][0], qf[nb][c * 4 + i][1]);
-        }
-      }
-    }
-    // scores in units of log2, masked
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const float s0 = f[nb][0] * md.sk[mt], s1 = f[nb][1] * md.sk[mt];
-        x[mt][nb][0] *= s0; x[mt][nb][1] *= s1; x[mt][nb][2] *= s0; x[mt][nb][3] *= s1;
-      }
-    if (t + kDecTile > clear || id.x < 0 || id.y < 0) {
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const bool gone = (mt == 0 ? id.x : id.y) < 0;
-        const int tt = t + mt * 16 + g;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          if (gone || tt >= see[nb][0]) x[mt][nb][0] = -INFINITY;
-          if (gone || tt >= see[nb][1]) x[mt][nb][1] = -INFINITY;
-          if (gone || tt + 8 >= see[nb][0]) x[mt][nb][2] = -INFINITY;
-          if (gone || tt + 8 >= see[nb][1]) x[mt][nb][3] = -INFINITY;
-        }
-      }
-    }
-    float top[NB][2];
-    bool grow = false;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float a = fmaxf(fmaxf(x[0][nb][i], x[0][nb][i + 2]), fmaxf(x[1][nb][i], x[1][nb][i + 2]));
-#pragma unroll
-        for (int s = 4; s < 32; s <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
-        top[nb][i] = fmaxf(m[nb][i], a);
-        grow = grow || top[nb][i] > m[nb][i];
-      }
-    const float vmax = fmaxf(vref, fmaxf(md.sv[0], md.sv[1]));
-    if (__any_sync(0xffffffffu, grow || vmax > vref)) {
-      const float fv = vmax > 0.0f ? __fdiv_rn(vref, vmax) : 1.0f;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        float b[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          b[i] = top[nb][i] == -INFINITY ? 1.0f : ex2(m[nb][i] - top[nb][i]);
-          l[nb][i] *= b[i];
-          m[nb][i] = top[nb][i];
-          b[i] *= fv;
-        }
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          o[j][nb][0] *= b[0]; o[j][nb][1] *= b[1]; o[j][nb][2] *= b[0]; o[j][nb][3] *= b[1];
-        }
-      }
-      vref = vmax;
-    }
-    const float rv = vref > 0.0f ? __fdiv_rn(1.0f, vref) : 0.0f;
-    uint32_t pb[2][NB][2];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const float z0 = m[nb][0] == -INFINITY ? 0.0f : m[nb][0], z1 = m[nb][1] == -INFINITY ? 0.0f : m[nb][1];
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const float wv = md.sv[mt] * rv;
-        const float p0 = ex2(x[mt][nb][0] - z0), p1 = ex2(x[mt][nb][1] - z1);
-        const float p2 = ex2(x[mt][nb][2] - z0), p3 = ex2(x[mt][nb][3] - z1);
-        l[nb][0] += p0 + p2;
-        l[nb][1] += p1 + p3;
-        // [token][row] -> [row][token]: the column operand of the second product
-        pb[mt][nb][0] = transpose8x8(pack_half2(p0 * wv, p1 * wv));
-        pb[mt][nb][1] = transpose8x8(pack_half2(p2 * wv, p3 * wv));
-      }
-    }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      uint32_t u[4][VW];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint8_t* row = vt + (s * 16 + 2 * q4 + (r & 1) + (r >> 1) * 8) * D + g * (D / 8);
-        if constexpr (D == 128) {
-          const uint4 w = *reinterpret_cast<const uint4*>(row);
-          u[r][0] = pre<FMT>(w.x); u[r][1] = pre<FMT>(w.y); u[r][2] = pre<FMT>(w.z); u[r][3] = pre<FMT>(w.w);
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(row);
-          u[r][0] = pre<FMT>(w.x); u[r][1] = pre<FMT>(w.y);
-        }
-      }
-      // accumulator tile j: operand row n is d = (D / 8) n + 2 j, row n + 8 the d after it
-#pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        const uint32_t la = __byte_perm(u[0][w], u[1][w], 0x5140), ha = __byte_perm(u[0][w], u[1][w], 0x7362);
-        const uint32_t lb = __byte_perm(u[2][w], u[3][w], 0x5140), hb = __byte_perm(u[2][w], u[3][w], 0x7362);
-        const uint32_t a0[4] = {half2_of<FMT, 0>(la), half2_of<FMT, 1>(la), half2_of<FMT, 0>(lb), half2_of<FMT, 1>(lb)};
-        const uint32_t a1[4] = {half2_of<FMT, 0>(ha), half2_of<FMT, 1>(ha), half2_of<FMT, 0>(hb), half2_of<FMT, 1>(hb)};
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          mma16816(o[2 * w][nb], a0, pb[s][nb][0], pb[s][nb][1]);
-          mma16816(o[2 * w + 1][nb], a1, pb[s][nb][0], pb[s][nb][1]);
-        }
-      }
-    }
+    S.step(kt, vt, wmeta[k & (2 * kDecGroup - 1)], wids[k & (2 * kDecGroup - 1)], t, lane);
     __syncwarp();
     if (k + NST < mine) issue(k + NST);
   }
   // join the four warps: weights 2^(m_w - M) and the value reference of each
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-      for (int s = 4; s < 32; s <<= 1) l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], s);
-      if (g == 0) wml[warp * NR + nb * 8 + 2 * q4 + i] = make_float2(m[nb][i], l[nb][i]);
-    }
-  if (lane == 0) s_vref[warp] = vref * kUnit<FMT>;
+  S.publish(wml + warp * NR, lane);
+  if (lane == 0) s_vref[warp] = S.vref;
   __syncthreads();                                       // every ring is free: the accumulators go there
   constexpr int AP = D + 4;                              // row pitch of the accumulators
   float* acc = reinterpret_cast<float*>(ring);           // [warp][NR][AP]
@@ -783,10 +850,9 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
       float* p = acc + (warp * NR + r) * AP + (D / 8) * g;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
-        *reinterpret_cast<float2*>(p + 2 * j) = make_float2(o[j][nb][i] * wt, o[j][nb][i + 2] * wt);
+        *reinterpret_cast<float2*>(p + 2 * j) = make_float2(S.o[j][nb][i] * wt, S.o[j][nb][i + 2] * wt);
     }
   __syncthreads();
-  const bool whole = !cluster && vis <= chunk;           // this CTA holds all that the rows see
   for (int idx = tid; idx < NR * D / 4; idx += kDecWarps * 32) {
     const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
     if (r >= R.rows) break;
@@ -801,19 +867,9 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
       const float4 y = *reinterpret_cast<const float4*>(acc + (w * NR + r) * AP + d);
       v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
     }
-    const int token = R.a + r / A.G, head = h * A.G + r % A.G;
-    if (cluster) {
-      *reinterpret_cast<float4*>(mine_o + r * D + d) = v;
-      if (d == 0) mine_ml[r] = make_float2(M, L);
-    } else if (whole) {
-      store_row4<DT>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + d, v, L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f);
-    } else {
-      const size_t cell = ((size_t)split * A.n_tokens + token) * A.heads + head;
-      *reinterpret_cast<float4*>(A.part_o + cell * D + d) = v;
-      if (d == 0) *reinterpret_cast<float2*>(A.part_ml + cell * 2) = make_float2(M, L);
-    }
+    *reinterpret_cast<float4*>(mine_o + r * D + d) = v;
+    if (d == 0) mine_ml[r] = make_float2(M, L);
   }
-  if (!cluster) return;
   // the cluster's CTAs in rank order, each taking its share of the values
   cluster_sync();
   const uint32_t o_at = smem_u32(mine_o), ml_at = smem_u32(mine_ml);
@@ -953,7 +1009,7 @@ struct Walk {
       const long long c = base + (A.causal ? (long long)cr * (r + 1) : 0);
       const int vis = seen_by(A, R, min(R.rows, (r + 1) * cr) - 1), tiles = (vis + kTileTok - 1) / kTileTok;
       const auto cut = [&](long long x) { return min(tiles, (int)((double)(x - s) * tiles / (double)c)); };
-      const int lo = s >= S.x0 ? 0 : cut(S.x0), hi = s + c <= S.x1 ? tiles : cut(S.x1);
+      const int lo = s >= S.x0 ? 0 : A.snap ? tiles : cut(S.x0), hi = s + c <= S.x1 || A.snap ? tiles : cut(S.x1);
       const bool mine = tiles == 0 ? s >= S.x0 : hi > lo;
       it = Item{req, h, R.a, R.n, R.L, R.rows, r * cr, lo, hi, lo == 0 && hi == tiles ? (int)kItemWhole : (lo == 0 ? 1 : 0), {hi, lo}};
       if (cr == kTileRows) {
@@ -987,6 +1043,183 @@ struct Walk {
   }
 };
 
+// Few rows on the balanced schedule: every CTA streams its share of all tokens, item
+// after item, the next item's tiles already on their way while one is finished.  A warp
+// takes the 32 tokens at 32 w of each 128-token tile.  Pieces of cut items go to the
+// workspace for paged_join_kernel; where A.snap is set items are not cut, and belong to
+// the CTA in whose share they start.
+template <int D, int NB>
+struct FlatSmem {
+  uint8_t ring[dec_ring_bytes(D)];
+  float sum[8 * NB][D];
+  __half q[8 * NB][D + 8];
+  DecMeta meta[kDecWarps][2 * kDecGroup];
+  int2 ids[kDecWarps][2 * kDecGroup];
+  float2 ml[kDecWarps][8 * NB];
+  float f[8 * NB];
+  float vref[kDecWarps];
+  uint64_t bars[kDecWarps][kDecStages];
+  int abort;
+};
+
+template <int DT, int FMT, int D, int NB>
+__global__ void __launch_bounds__(kDecWarps * 32) paged_flat_kernel(const AttnArgs A) {
+  constexpr int NST = kDecStages, kStage = dec_stage_bytes(D), NR = 8 * NB;
+  extern __shared__ __align__(128) uint8_t dsm[];
+  FlatSmem<D, NB>& X = *reinterpret_cast<FlatSmem<D, NB>*>(dsm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    X.abort = 0;
+    for (int s = 0; s < kDecWarps * NST; ++s) mbar_init(&X.bars[0][0] + s, 1);
+    fence_mbar_init();
+  }
+  griddep_wait();
+  griddep_launch();
+  const Share share = cta_share<kDecWarps * 32>(A, NR, blockIdx.x, gridDim.x);   // ends with a barrier
+  if (tid < 2 && A.pieces) A.pieces[blockIdx.x * 2 + tid].valid = 0;
+  __syncthreads();
+  if (share.req < 0) return;
+  uint8_t* ring = X.ring + warp * NST * kStage;
+  uint64_t* bar = X.bars[warp];
+  DecMeta* meta = X.meta[warp];
+  int2* ids = X.ids[warp];
+  const size_t blk_bytes = (size_t)(D << A.lb);
+  const auto end_of = [&](const Item& I) {                 // tokens that the piece's rows see
+    const Rows R = {I.a, I.n, I.L, I.rows};
+    return min(seen_by(A, R, I.rows - 1), I.hi * kTileTok);
+  };
+
+  // the tiles on their way: `sent` so far, the next one at token `t` of the item below `t_end`
+  Walk ahead;
+  ahead.start(A, share, NR);
+  int sent = 0, t = 0, t_end = 0, h = 0, grouped = 0;
+  const int* row = nullptr;
+  const auto send = [&]() {
+    while (t >= t_end) {
+      Item I;
+      if (!ahead.next(A, share, NR, I)) { t = 0; t_end = -1; return; }
+      t = I.lo * kTileTok + 32 * warp;
+      t_end = end_of(I);
+      h = I.h;
+      row = A.table + (size_t)I.req * A.max_blocks;
+      grouped = 0;
+    }
+    if (grouped == 0) {                                    // block numbers and scales of the next tiles, a lane each
+      const int tt = t + lane * kTileTok;
+      if (lane < kDecGroup) {
+        int2 id = make_int2(-1, -1);
+        DecMeta m = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+        if (tt < t_end) {
+          const int nblk = blocks_of(t_end, A.lb), c0 = tt >> A.lb, c1 = (tt + 16) >> A.lb;
+          id.x = row[c0];
+          id.y = c1 == c0 ? id.x : (c1 < nblk ? row[c1] : -2);
+          if (id.x < 0 || id.x >= A.n_blocks) { id.x = -1; record_status(SVDQ_ERR_INVALID_ARG); }
+          if (id.y != -2 && (id.y < 0 || id.y >= A.n_blocks)) { id.y = -1; record_status(SVDQ_ERR_INVALID_ARG); }
+          if (id.x >= 0) { const size_t c = (size_t)id.x * A.kv + h; m.sk[0] = A.ks[c]; m.sv[0] = A.vs[c]; }
+          if (id.y >= 0) { const size_t c = (size_t)id.y * A.kv + h; m.sk[1] = A.ks[c]; m.sv[1] = A.vs[c]; }
+        }
+        ids[(sent + lane) & (2 * kDecGroup - 1)] = id;
+        meta[(sent + lane) & (2 * kDecGroup - 1)] = m;
+      }
+      grouped = kDecGroup;
+      __syncwarp();
+    }
+    if (lane == 0) {
+      const int o = t & ((1 << A.lb) - 1);
+      const int2 id = ids[sent & (2 * kDecGroup - 1)];
+      uint8_t* dst = ring + (sent % NST) * kStage;
+      uint64_t* b = &bar[sent % NST];
+      const int x = A.lb >= 5 ? 2 : 1;                     // halves of a tile that one copy brings
+      mbar_arrive_expect_tx(b, ((id.x >= 0 ? x : 0) + (x == 1 && id.y >= 0 ? 1 : 0)) * 32 * D);
+      if (id.x >= 0) {
+        const size_t at = ((size_t)id.x * A.kv + h) * blk_bytes + (size_t)o * D;
+        bulk_load(dst, A.kc + at, 16 * x * D, b);
+        bulk_load(dst + kDecTile * D, A.vc + at, 16 * x * D, b);
+      }
+      if (x == 1 && id.y >= 0) {
+        const size_t at = ((size_t)id.y * A.kv + h) * blk_bytes;
+        bulk_load(dst + 16 * D, A.kc + at, 16 * D, b);
+        bulk_load(dst + kDecTile * D + 16 * D, A.vc + at, 16 * D, b);
+      }
+    }
+    ++sent;
+    --grouped;
+    t += kTileTok;
+  };
+  for (int s = 0; s < NST; ++s) send();
+
+  Walk walk;
+  walk.start(A, share, NR);
+  Item I;
+  int done = 0;
+  bool dead = false;
+  RowState<FMT, D, NB> S;
+  while (walk.next(A, share, NR, I)) {
+    const Rows R = {I.a, I.n, I.L, I.rows};
+    const int end = end_of(I);
+    load_queries<DT, D>(A, R, I.h, 0, NR, &X.q[0][0], X.f, warp, kDecWarps, lane);
+    __syncthreads();
+    S.start(A, R, &X.q[0][0], X.f, end, lane);
+    for (int at = I.lo * kTileTok + 32 * warp; at < end && !dead; at += kTileTok, ++done) {
+      if (!mbar_wait(&bar[done % NST], (done / NST) & 1, &X.abort)) {
+        int own = 0;                                       // the copies in flight end before the CTA does
+        for (int i = done; i < sent; ++i) mbar_wait(&bar[i % NST], (i / NST) & 1, &own);
+        dead = true;
+        break;
+      }
+      const uint8_t* kt = ring + (done % NST) * kStage;
+      S.step(kt, kt + kDecTile * D, meta[done & (2 * kDecGroup - 1)], ids[done & (2 * kDecGroup - 1)], at, lane);
+      __syncwarp();
+      send();
+    }
+    // join the four warps in order: weights 2^(m_w - M) and the value reference of each
+    S.publish(X.ml[warp], lane);
+    if (lane == 0) X.vref[warp] = S.vref;
+    __syncthreads();
+    const auto top = [&](int r) { return fmaxf(fmaxf(X.ml[0][r].x, X.ml[1][r].x), fmaxf(X.ml[2][r].x, X.ml[3][r].x)); };
+    const auto weight = [&](int w, int r, float M) { const float x = X.ml[w][r].x; return x == -INFINITY ? 0.0f : ex2(x - M); };
+    static_assert(kDecWarps == 4, "the join is written for four warps");
+#pragma unroll 1
+    for (int w = 0; w < kDecWarps; ++w) {
+      if (warp == w) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = nb * 8 + 2 * (lane & 3) + i;
+            const float wt = weight(w, r, top(r)) * X.vref[w];
+            float2* p = reinterpret_cast<float2*>(&X.sum[r][(D / 8) * (lane >> 2)]);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              const float2 v = w == 0 ? make_float2(0.0f, 0.0f) : p[j];
+              p[j] = make_float2(v.x + S.o[j][nb][i] * wt, v.y + S.o[j][nb][i + 2] * wt);
+            }
+          }
+      }
+      __syncthreads();
+    }
+    const int tiles = (seen_by(A, R, R.rows - 1) + kTileTok - 1) / kTileTok;
+    if (tid == 0 && I.out != kItemWhole) A.pieces[blockIdx.x * 2 + I.out] = Piece{1, I.hi == tiles, I.a, I.rows, I.h, 0, 0, 0};
+    for (int idx = tid; idx < NR * D / 4; idx += kDecWarps * 32) {
+      const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
+      if (r >= R.rows) break;
+      const float M = top(r);
+      float L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) L += weight(w, r, M) * X.ml[w][r].y;
+      const float4 v = *reinterpret_cast<const float4*>(&X.sum[r][d]);
+      if (I.out == kItemWhole) {
+        const int token = R.a + r / A.G, head = I.h * A.G + r % A.G;
+        store_row4<DT>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + d, v, L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f);
+      } else {
+        const size_t cell = ((size_t)blockIdx.x * 2 + I.out) * NR + r;
+        *reinterpret_cast<float4*>(A.part_o + cell * D + d) = v;
+        if (d == 0) *reinterpret_cast<float2*>(A.part_ml + cell * 2) = make_float2(M, L);
+      }
+    }
+  }
+}
+
 // Many rows: items of 256 rows (two tiles of 128) on the tensor cores, one CTA per SM
 // that works through its share without a break between items.  Codes become fp16
 // operands in shared memory once per 128 tokens and serve both row tiles: S = Q K^T
@@ -1010,7 +1243,6 @@ constexpr int tile_bytes(int D) { return D / 64 * kTileHalf; }
 constexpr int tiles_smem(int D) {
   return 6 * tile_bytes(D) + kTileRows * 4 + kTileMeta * 8 * 16 + kItems * (int)sizeof(Item) + 512 + 1024;
 }
-constexpr float kGrow = 7.0f;
 
 // MN-major operand with the 128-byte swizzle: rows of 64 values (128 bytes) along K,
 // 8-row groups 1024 bytes apart, the next 64 values of MN kTileHalf further.
@@ -1580,48 +1812,49 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
 
 // Adds the pieces of the items that a border of the schedule cut: blockIdx.x is the
 // CTA whose last item continues in the CTAs after it, blockIdx.y a part of its rows,
-// a warp per row.  Pieces are added in the order of their tokens.
+// `wide` warps a row (warp w of them takes every wide-th piece; then the warps in
+// order).  One warp a row where an item has a few pieces, all eight where a long
+// request is cut over many CTAs (55 pieces: 25 -> 4 us).
 constexpr int kJoinWarps = 8, kMaxParts = 1024;
 template <int DT, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnArgs A, int parts, int cr) {
-  constexpr int V = D / 32;                              // values a lane
-  __shared__ uint8_t s_state[kMaxParts];                 // bit 0: holds a piece, bit 1: the item's last
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnArgs A, int parts, int rows, int wide) {
+  constexpr int V = D / 32, kAhead = 4;                  // values a lane, pieces in flight
+  __shared__ uint8_t s_valid[kMaxParts];
+  __shared__ int s_last;
+  __shared__ float s_v[kJoinWarps][D];
+  __shared__ float2 s_ml[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x;
   griddep_wait();
   const Piece P = A.pieces[c0 * 2 + 1];
   if (!P.valid) return;
-  for (int k = c0 + 1 + threadIdx.x; k < parts; k += kJoinWarps * 32)
-    s_state[k] = (uint8_t)(A.pieces[k * 2].valid | A.pieces[k * 2].last << 1);
+  if (threadIdx.x == 0) s_last = parts - 1;
   __syncthreads();
-  for (int r = blockIdx.y * kJoinWarps + warp; r < P.n_rows; r += gridDim.y * kJoinWarps) {
+  for (int k = c0 + 1 + threadIdx.x; k < parts; k += kJoinWarps * 32) {
+    const int valid = A.pieces[k * 2].valid;
+    s_valid[k] = (uint8_t)valid;
+    if (valid && A.pieces[k * 2].last) atomicMin(&s_last, k);   // the first last one ends this item
+  }
+  __syncthreads();
+  const int last = s_last, per = kJoinWarps / wide, sub = warp % wide;
+  for (int r0 = blockIdx.y * per; r0 < P.n_rows; r0 += gridDim.y * per) {
+    const int r = r0 + warp / wide;
+    const bool mine = r < P.n_rows;
     float m = -INFINITY, l = 0.0f, v[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = 0.0f;
-    int k = c0, next = c0 + 1;
-    while (k >= 0) {
-      // four pieces at a time: loads first
-      size_t cell[4];
-      int n = 0;
+    for (int k0 = c0 + sub; mine && k0 <= last; k0 += kAhead * wide) {
+      float2 ml[kAhead];
+      float x[kAhead][V], top = m;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (k >= 0) {
-          cell[b] = ((size_t)k * 2 + (k == c0)) * cr + r;
-          n = b + 1;
-          const bool end = k != c0 && (s_state[k] & 2);
-          while (!end && next < parts && !(s_state[next] & 1)) ++next;
-          k = end || next >= parts ? -1 : next++;
-        }
-      }
-      float2 ml[4];
-      float x[4][V], top = m;
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
+      for (int b = 0; b < kAhead; ++b) {
+        const int k = k0 + b * wide;
         ml[b] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
         for (int i = 0; i < V; ++i) x[b][i] = 0.0f;
-        if (b < n) {
-          ml[b] = *reinterpret_cast<const float2*>(A.part_ml + cell[b] * 2);
-          const float* src = A.part_o + cell[b] * D + V * lane;
+        if (k <= last && (k == c0 || s_valid[k])) {
+          const size_t cell = ((size_t)k * 2 + (k == c0)) * rows + r;
+          ml[b] = *reinterpret_cast<const float2*>(A.part_ml + cell * 2);
+          const float* src = A.part_o + cell * D + V * lane;
           if constexpr (V == 4) {
             const float4 y = *reinterpret_cast<const float4*>(src);
             x[b][0] = y.x; x[b][1] = y.y; x[b][2] = y.z; x[b][3] = y.w;
@@ -1630,21 +1863,44 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnA
             x[b][0] = y.x; x[b][1] = y.y;
           }
         }
-        top = fmaxf(top, ml[b].x);
       }
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) top = fmaxf(top, ml[b].x);
       const float back = m == -INFINITY ? 0.0f : ex2(m - top);
       m = top;
       l *= back;
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] *= back;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
+      for (int b = 0; b < kAhead; ++b) {
         const float w = ml[b].x == -INFINITY ? 0.0f : ex2(ml[b].x - m);
         l += w * ml[b].y;
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] += w * x[b][i];
       }
     }
+    if (wide > 1) {
+      __syncthreads();                                   // the row before is read
+      if (lane == 0) s_ml[warp] = make_float2(m, l);
+#pragma unroll
+      for (int i = 0; i < V; ++i) s_v[warp][V * lane + i] = v[i];
+      __syncthreads();
+      if (sub > 0) continue;
+      float M = m;
+      for (int w = 1; w < wide; ++w) M = fmaxf(M, s_ml[warp + w].x);
+      const float own = m == -INFINITY ? 0.0f : ex2(m - M);
+      l *= own;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= own;
+      for (int w = 1; w < wide; ++w) {
+        const float2 ml = s_ml[warp + w];
+        const float b = ml.x == -INFINITY ? 0.0f : ex2(ml.x - M);
+        l += b * ml.y;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += b * s_v[warp + w][V * lane + i];
+      }
+    }
+    if (!mine) continue;
     const int row = P.r0 + r;
     const float mul = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
     uint16_t* dst = A.out + (int64_t)(P.token + row / A.G) * A.out_stride + (int64_t)(P.h * A.G + row % A.G) * D + V * lane;
@@ -1654,68 +1910,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnA
     if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(dst) = w[0];
   }
-}
-
-// Joins the splits of a row in a fixed order: a CTA per row, warp w takes splits w,
-// w + 4, ..., then the warps in order.  Rows whose tokens fitted one split were
-// written already.
-template <int DT, int D>
-__global__ void __launch_bounds__(128) paged_join_splits_kernel(const AttnArgs A, int tile_rows) {
-  constexpr int V = D / 32;                              // values a lane
-  __shared__ float s_v[4][D], s_m[4], s_l[4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.x, h = blockIdx.y, req = blockIdx.z;
-  griddep_wait();
-  const Rows R = request_rows(A, req, threadIdx.x == 0);
-  if (r >= R.rows) return;
-  const int vis = seen_by(A, R, min(R.rows, (r / tile_rows + 1) * tile_rows) - 1);
-  if (vis <= A.chunk) return;
-  const int n = (vis + A.chunk - 1) / A.chunk;
-  const int token = R.a + r / A.G, head = h * A.G + r % A.G;
-  const size_t cell = (size_t)token * A.heads + head, step = (size_t)A.n_tokens * A.heads;
-  float m = -INFINITY, l = 0.0f, v[V];
-#pragma unroll
-  for (int k = 0; k < V; ++k) v[k] = 0.0f;
-  for (int s0 = warp; s0 < n; s0 += 8 * 4) {
-    float2 ml[8];
-    float x[8][V], top = m;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int s = s0 + i * 4;
-      const size_t c = cell + (size_t)s * step;
-      ml[i] = s < n ? *reinterpret_cast<const float2*>(A.part_ml + c * 2) : make_float2(-INFINITY, 0.0f);
-#pragma unroll
-      for (int k = 0; k < V; ++k) x[i][k] = s < n ? A.part_o[c * D + V * lane + k] : 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, ml[i].x);
-    const float b = m == -INFINITY ? 0.0f : ex2(m - top);
-    m = top;
-    l *= b;
-#pragma unroll
-    for (int k = 0; k < V; ++k) v[k] *= b;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float w = ml[i].x == -INFINITY ? 0.0f : ex2(ml[i].x - m);
-      l += w * ml[i].y;
-#pragma unroll
-      for (int k = 0; k < V; ++k) v[k] += w * x[i][k];
-    }
-  }
-  if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
-#pragma unroll
-  for (int k = 0; k < V; ++k) s_v[warp][V * lane + k] = v[k];
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  float M = -INFINITY, L = 0.0f, y = 0.0f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w]);
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float b = s_m[w] == -INFINITY ? 0.0f : ex2(s_m[w] - M);
-    L += b * s_l[w];
-    y += b * s_v[w][threadIdx.x];
-  }
-  A.out[(int64_t)token * A.out_stride + (int64_t)head * D + threadIdx.x] = store16<DT>(L > 0.0f ? __fdiv_rn(y, L) : 0.0f);
 }
 
 // ------------------------------------------------------------- host launchers
@@ -1766,6 +1960,8 @@ cudaError_t attention_attr() {
   const auto smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
   cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<DT, FMT, D, 1>, smem, dec_smem(D, 1));
   if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_rows_kernel<DT, FMT, D, 2>, smem, dec_smem(D, 2));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_flat_kernel<DT, FMT, D, 1>, smem, (int)sizeof(FlatSmem<D, 1>));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_flat_kernel<DT, FMT, D, 2>, smem, (int)sizeof(FlatSmem<D, 2>));
   if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_tiles_kernel<DT, FMT, D>, smem, tiles_smem(D));
   return e;
 }
@@ -1806,112 +2002,99 @@ svdq_status device_ready(int* sms) {
   return state == 1 ? SVDQ_OK : SVDQ_ERR_UNSUPPORTED;
 }
 
-svdq_status launched(const char* where) {
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? SVDQ_OK : cuda_failure(e, where);
-}
-
 // The SM count that the split aims at: fixed, so that workspace sizes can be asked
 // for without a device.
 constexpr int kSplitSms = 148;
-constexpr int kMinTiles = 1;
 
-// How a call's rows and tokens are split: CTAs of `cta_rows` rows (8, 16: the few-row
-// kernel; 128, 256: the tensor-core kernel) x `splits` ranges of tokens.  Up to
-// kMaxCluster splits of the few-row kernel form a cluster, which shares each
-// request's tokens evenly and joins in shared memory; otherwise a split is `chunk`
-// tokens (a multiple of 128) and a second kernel joins them through the workspace.
-struct Split { int cta_rows, row_ctas, splits, chunk, cluster; };
-Split split_of(const svdq_paged_cache* c, const svdq_paged_batch* b, int sms) {
-  Split s;
-  const int64_t rows = (int64_t)b->max_new * (c->heads / c->kv_heads), cells = (int64_t)b->B * c->kv_heads;
-  const auto ctas = [&](int per) { return (rows + per - 1) / per * cells; };
-  const int64_t len = std::max(b->max_len, 1);
-  if (rows <= 16) {
-    s.cta_rows = rows <= 8 ? 8 : 16;
-    s.row_ctas = 1;
-    const int64_t unit = kDecWarps * kDecTile, want = std::min((4 * sms + cells - 1) / cells, (len + 2 * unit - 1) / (2 * unit));
-    s.cluster = want > 1 && want <= kMaxCluster;
-    s.splits = s.cluster ? (want > 4 ? 8 : want > 2 ? 4 : 2) : (int)std::max<int64_t>(1, want);
-    s.chunk = (int)(((len + s.splits - 1) / s.splits + unit - 1) / unit * unit);
-    if (!s.cluster) s.splits = (int)((len + s.chunk - 1) / s.chunk);
-    return s;
+// How a call's rows and tokens are split.  Up to 16 rows a request (few-row kernels,
+// rows 8 or 16): fewer (request, kv head) cells than SMs take a cluster of up to
+// kMaxCluster CTAs each, as long as those fill the chip; otherwise the balanced schedule
+// over as many CTAs as are resident at once.  More rows: the tensor-core kernel (rows
+// 256), a CTA per SM.  No CTA of a schedule is left with less than a token tile.
+struct Split { int rows, ctas, cluster, snap; };
+constexpr int flat_per_sm(int head_dim, int rows) { return head_dim == 64 ? 4 : rows == 8 ? 3 : 2; }
+Split split_of(const svdq_paged_cache* c, const svdq_paged_batch* b) {
+  const int64_t G = c->heads / c->kv_heads, rows = b->max_new * G, cells = (int64_t)b->B * c->kv_heads;
+  const int64_t len = std::max(b->max_len, 1), tiles = (len + kTileTok - 1) / kTileTok;
+  const auto within = [](int64_t n, int64_t hi) { return (int)std::clamp<int64_t>(n, 1, hi); };
+  if (rows > 16) {
+    const int64_t items = std::min((rows + kTileRows - 1) / kTileRows * b->B, b->n_tokens * G / kTileRows + b->B) * c->kv_heads;
+    return Split{kTileRows, within(items * tiles, kSplitSms), 0, 0};
   }
-  // one CTA per SM, fewer where that leaves one less than kMinTiles token tiles
-  const int64_t items = std::min(ctas(kTileRows), ((int64_t)b->n_tokens * (c->heads / c->kv_heads) / kTileRows + b->B) * c->kv_heads);
-  const int64_t tiles = items * ((len + kTileTok - 1) / kTileTok);
-  s = Split{kTileRows, 0, (int)std::clamp<int64_t>(tiles / kMinTiles, 1, sms), 0, 0};
-  return s;
+  const int nr = rows <= 8 ? 8 : 16;
+  const int64_t want = std::min((4 * kSplitSms + cells - 1) / cells, (len + 255) / 256);
+  if (cells < kSplitSms && want <= kMaxCluster) return Split{nr, want > 4 ? 8 : want > 2 ? 4 : (int)want, 1, 0};
+  // whole items where they are short: a cut costs a second kernel, an uneven share at most two tiles
+  return Split{nr, within(cells * tiles, (int64_t)kSplitSms * flat_per_sm(c->head_dim, nr)), 0, tiles <= 2};
 }
+bool joins(const Split& s) { return !s.cluster && !s.snap && s.ctas > 1; }
 
 size_t attention_ws(const svdq_paged_cache* c, const svdq_paged_batch* b) {
-  const Split s = split_of(c, b, kSplitSms);
-  if (s.splits <= 1 || s.cluster) return 16;
-  if (s.cta_rows == kTileRows) return (size_t)s.splits * 2 * (sizeof(Piece) + kTileRows * (size_t)(c->head_dim + 2) * sizeof(float));
-  return (size_t)s.splits * b->n_tokens * c->heads * (size_t)(c->head_dim + 2) * sizeof(float);
+  const Split s = split_of(c, b);
+  return joins(s) ? (size_t)s.ctas * 2 * (sizeof(Piece) + s.rows * (size_t)(c->head_dim + 2) * sizeof(float)) : 16;
 }
 
 // A launch that may start while the kernel before it on the stream still runs (each
 // kernel waits for that one before it touches memory).
 template <class... P, class... Q>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, const Q&... args) {
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, int cluster, const Q&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int DT, int FMT, int D, int NB>
-cudaError_t launch_rows(const AttnArgs& A, const Split& s, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)s.splits, (unsigned)A.kv, (unsigned)A.B);
-  cfg.blockDim = dim3(kDecWarps * 32);
-  cfg.dynamicSmemBytes = dec_smem(D, NB);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)(s.cluster ? s.splits : 1);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_rows_kernel<DT, FMT, D, NB>, A, s.cluster);
+svdq_status launch_few(const AttnArgs& A, const Split& s, cudaStream_t stream) {
+  cudaError_t e;
+  if (s.cluster) {
+    e = launch_after(paged_rows_kernel<DT, FMT, D, NB>, dim3((unsigned)s.ctas, (unsigned)A.kv, (unsigned)A.B), kDecWarps * 32,
+                     dec_smem(D, NB), stream, s.ctas, A);
+    return e == cudaSuccess ? SVDQ_OK : cuda_failure(e, "paged_rows_kernel launch");
+  }
+  e = launch_after(paged_flat_kernel<DT, FMT, D, NB>, dim3((unsigned)s.ctas), kDecWarps * 32, (int)sizeof(FlatSmem<D, NB>), stream, 1, A);
+  return e == cudaSuccess ? SVDQ_OK : cuda_failure(e, "paged_flat_kernel launch");
 }
 
 template <int DT, int FMT, int D>
 svdq_status launch_attention(const AttnArgs& A, const Split& s, cudaStream_t stream) {
   cudaError_t e;
-  if (s.cta_rows <= 16) {
-    e = s.cta_rows == 8 ? launch_rows<DT, FMT, D, 1>(A, s, stream) : launch_rows<DT, FMT, D, 2>(A, s, stream);
-    if (e != cudaSuccess) return cuda_failure(e, "paged_rows_kernel launch");
+  if (s.rows < kTileRows) {
+    const svdq_status st = s.rows == 8 ? launch_few<DT, FMT, D, 1>(A, s, stream) : launch_few<DT, FMT, D, 2>(A, s, stream);
+    if (st != SVDQ_OK) return st;
   } else {
-    e = launch_after(paged_tiles_kernel<DT, FMT, D>, dim3((unsigned)s.splits), kTileThreads, tiles_smem(D), stream, A);
+    e = launch_after(paged_tiles_kernel<DT, FMT, D>, dim3((unsigned)s.ctas), kTileThreads, tiles_smem(D), stream, 1, A);
     if (e != cudaSuccess) return cuda_failure(e, "paged_tiles_kernel launch");
-    if (s.splits <= 1) return SVDQ_OK;
-    e = launch_after(paged_join_kernel<DT, D>, dim3((unsigned)s.splits, 8u), kJoinWarps * 32, 0, stream, A, s.splits, kTileRows);
-    return e == cudaSuccess ? SVDQ_OK : cuda_failure(e, "paged_join_kernel launch");
   }
-  if (s.splits <= 1 || s.cluster) return SVDQ_OK;
-  e = launch_after(paged_join_splits_kernel<DT, D>, dim3((unsigned)(A.max_new * A.G), (unsigned)A.kv, (unsigned)A.B), 128, 0, stream, A, s.cta_rows);
-  return e == cudaSuccess ? SVDQ_OK : cuda_failure(e, "paged_join_splits_kernel launch");
+  if (!joins(s)) return SVDQ_OK;
+  const int64_t all = (int64_t)A.max_new * A.G, items = (all + s.rows - 1) / s.rows * A.B * A.kv;
+  const int real = (int)std::min<int64_t>(s.rows, all), wide = s.ctas >= 8 * items ? kJoinWarps : 1, per = kJoinWarps / wide;
+  const dim3 grid((unsigned)s.ctas, (unsigned)std::min(32, (real + per - 1) / per));
+  e = launch_after(paged_join_kernel<DT, D>, grid, kJoinWarps * 32, 0, stream, 1, A, s.ctas, s.rows, wide);
+  return e == cudaSuccess ? SVDQ_OK : cuda_failure(e, "paged_join_kernel launch");
 }
 
 template <int DT, int FMT, int D>
 svdq_status launch_append(const AppendArgs& A, int lb, dim3 grid, cudaStream_t s) {
+  cudaError_t e;
   switch (lb) {
-    case 4: paged_append_kernel<DT, FMT, D, 4><<<grid, kAppendThreads, 0, s>>>(A); break;
-    case 5: paged_append_kernel<DT, FMT, D, 5><<<grid, kAppendThreads, 0, s>>>(A); break;
-    case 6: paged_append_kernel<DT, FMT, D, 6><<<grid, kAppendThreads, 0, s>>>(A); break;
-    default: paged_append_kernel<DT, FMT, D, 7><<<grid, kAppendThreads, 0, s>>>(A); break;
+    case 4: e = launch_after(paged_append_kernel<DT, FMT, D, 4>, grid, append_threads(16, D), 0, s, 1, A); break;
+    case 5: e = launch_after(paged_append_kernel<DT, FMT, D, 5>, grid, append_threads(32, D), 0, s, 1, A); break;
+    case 6: e = launch_after(paged_append_kernel<DT, FMT, D, 6>, grid, append_threads(64, D), 0, s, 1, A); break;
+    default: e = launch_after(paged_append_kernel<DT, FMT, D, 7>, grid, append_threads(128, D), 0, s, 1, A); break;
   }
-  return launched("paged_append_kernel launch");
+  return e == cudaSuccess ? SVDQ_OK : cuda_failure(e, "paged_append_kernel launch");
 }
 
 // The call's dtype, format and head size as template arguments.
@@ -1985,8 +2168,9 @@ svdq_status svdq_paged_plan(const svdq_paged_batch* b, int32_t block_size, int32
   A.n_blocks = n_blocks; A.lb = lb;
   // a CTA per 2048 slots: up to there one CTA's scan and writes are cheaper than another CTA's scan
   const int ctas = (int)std::min<int64_t>(sms, std::max<int64_t>(1, ((int64_t)b->n_tokens + b->B + 2047) / 2048));
-  paged_plan_kernel<<<ctas, kPlanThreads, plan_smem_bytes(b->B), reinterpret_cast<cudaStream_t>(stream)>>>(A);
-  return launched("paged_plan_kernel launch");
+  const cudaError_t e = launch_after(paged_plan_kernel, dim3((unsigned)ctas), kPlanThreads, plan_smem_bytes(b->B),
+                                     reinterpret_cast<cudaStream_t>(stream), 1, A);
+  return e == cudaSuccess ? SVDQ_OK : cuda_failure(e, "paged_plan_kernel launch");
 }
 
 svdq_status svdq_paged_append(const svdq_paged_cache* c, const svdq_paged_batch* b, const void* K, int64_t k_stride,
@@ -2006,8 +2190,9 @@ svdq_status svdq_paged_append(const svdq_paged_cache* c, const svdq_paged_batch*
   A.stride[0] = k_stride; A.stride[1] = v_stride;
   A.codes[0] = c->kcodes; A.codes[1] = c->vcodes; A.scale[0] = c->kscale; A.scale[1] = c->vscale;
   A.cu = b->cu; A.slots = b->slots; A.B = b->B; A.n_tokens = b->n_tokens; A.kv = c->kv_heads; A.n_blocks = c->n_blocks;
+  A.max_new = b->max_new; A.per = b->max_new == 1 ? 1 : 2;
   const int lb = log2_block(c->block_size);
-  const dim3 grid((unsigned)((b->n_tokens >> lb) + 2 * b->B), (unsigned)c->kv_heads, 2u);
+  const dim3 grid((unsigned)((b->n_tokens >> lb) + A.per * b->B), (unsigned)c->kv_heads, 2u);
   return by_types(c, AppendCall{A, lb, grid, reinterpret_cast<cudaStream_t>(stream)});
 }
 
@@ -2032,25 +2217,24 @@ svdq_status svdq_paged_attention(const svdq_paged_cache* c, const svdq_paged_bat
     return SVDQ_ERR_ALIGNMENT;
   int sms = 0;
   if ((st = device_ready(&sms)) != SVDQ_OK) return st;
-  const Split sp = split_of(c, b, kSplitSms);
+  const Split sp = split_of(c, b);
   AttnArgs A;
   A.q = static_cast<const uint16_t*>(Q); A.out = static_cast<uint16_t*>(out);
   A.kc = c->kcodes; A.vc = c->vcodes; A.ks = c->kscale; A.vs = c->vscale;
   A.table = b->table; A.lens = b->lens; A.cu = b->cu;
-  A.part_o = static_cast<float*>(workspace);
-  A.part_ml = A.part_o + (size_t)sp.splits * b->n_tokens * c->heads * c->head_dim;
   A.pieces = nullptr;
-  if (sp.cta_rows == kTileRows && sp.splits > 1) {
+  A.part_ml = A.part_o = nullptr;
+  if (joins(sp)) {
     A.pieces = static_cast<Piece*>(workspace);
-    A.part_ml = reinterpret_cast<float*>(A.pieces + sp.splits * 2);
-    A.part_o = A.part_ml + (size_t)sp.splits * 2 * kTileRows * 2;
+    A.part_ml = reinterpret_cast<float*>(A.pieces + sp.ctas * 2);
+    A.part_o = A.part_ml + (size_t)sp.ctas * 2 * sp.rows * 2;
   }
   A.q_stride = q_stride; A.out_stride = out_stride;
   A.B = b->B; A.max_blocks = b->max_blocks; A.n_tokens = b->n_tokens; A.max_new = b->max_new; A.max_len = b->max_len;
   A.n_blocks = c->n_blocks; A.heads = c->heads; A.kv = c->kv_heads; A.G = c->heads / c->kv_heads;
-  A.lb = log2_block(c->block_size); A.causal = causal; A.splits = sp.splits; A.chunk = sp.chunk;
+  A.lb = log2_block(c->block_size); A.causal = causal; A.splits = sp.ctas; A.snap = sp.snap;
   A.scale_log2 = scale * 1.4426950408889634f;
-  A.inv_parts = 1.0 / sp.splits;
+  A.inv_parts = 1.0 / sp.ctas;
   A.g_inv = A.G == 1 ? 0u : (uint32_t)(((1ull << 32) + A.G - 1) / A.G);
   return by_types(c, AttnCall{A, sp, reinterpret_cast<cudaStream_t>(stream)});
 }
