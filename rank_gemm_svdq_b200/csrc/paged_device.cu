@@ -1364,16 +1364,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
     mbar_init(drained, 1);
     fence_mbar_init();
   }
+  griddep_wait();
+  // TMEM only now: a kernel before this one may still want its own, and would wait for ours
   if (warp == 12) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
   }
-  griddep_wait();
-  griddep_launch();
   const Share share = cta_share<kTileThreads>(A, kTileRows, blockIdx.x, gridDim.x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_launch();
   const uint32_t tm = s_tmem;
   // the k-th item, for one warp: false when there are no more; done with it: give_back
   const auto take = [&](int k) {

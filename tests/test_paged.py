@@ -438,3 +438,219 @@ def test_attention_matches_oracle(gpu, heads, kv, d, bs, new, lens, fmt, dtype, 
     if causal and new[0] > lens[0] and want.size:
         assert not want[: new[0] - lens[0]].any()          # rows that see nothing are zero
     assert sv.get_status() == sv.OK
+
+
+# Shapes that reach each way of sharing the work out: (heads, kv, d, bs, new, lens)
+def ragged(seed, B, lo, hi, new=1, idle=0.0):
+    r = random.Random(seed)
+    lens = [r.randint(lo, hi) for _ in range(B)]
+    return [0 if r.random() < idle else min(new, L) if new == 1 else r.randint(1, min(new, max(L, 1))) for L in lens], lens
+
+
+SCHEDULE = [
+    (8, 4, 128, 64, *ragged(1, 48, 1, 900)),               # more cells than SMs: shares cut inside requests
+    (16, 8, 64, 16, *ragged(2, 40, 1, 700, 4)),            # 8 rows of several tokens
+    (64, 4, 128, 32, *ragged(3, 40, 1, 600)),              # 16 rows
+    (5, 5, 64, 128, *ragged(4, 200, 1, 250)),              # short: whole items
+    (4, 4, 128, 16, *ragged(5, 130, 1, 300, 1, 0.9)),      # most requests idle
+    (2, 1, 128, 128, [1], [9000]),                         # one long request over the whole chip
+    (1, 1, 64, 16, [3], [7000]),
+    (20, 1, 128, 64, [1], [6000]),                         # 20 rows over the whole chip
+    (3, 3, 64, 32, *ragged(6, 70, 1, 400, 90, 0.5)),       # tensor-core rows, half the requests idle
+    (200, 1, 128, 16, [3, 1], [333, 40]),                  # many heads on one
+    (7, 1, 64, 64, [90, 1, 200], [90, 64, 1500])]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,d,bs,new,lens", SCHEDULE)
+@pytest.mark.parametrize("fmt,dtype,causal", [("int8", "bf16", True), ("e4m3", "fp16", True), ("e4m3", "bf16", False)])
+def test_attention_schedules(gpu, heads, kv, d, bs, new, lens, fmt, dtype, causal):
+    P = Pool(sum(lens) + heads, heads, kv, d, bs, sum(-(-L // bs) for L in lens) + 2, fmt, dtype)
+    table = make_table(P.rng, lens, bs, P.n, max(-(-L // bs) for L in lens) + 1, fill=-1)
+    spoil(P, table, lens)
+    run_attend(P, new, lens, causal, dtype, table)
+    assert sv.get_status() == sv.OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,d,bs,new,lens", [
+    (4, 2, 128, 64, [1, 1], [300, 90]), (4, 4, 64, 16, [1] * 40, [100] * 40), (8, 2, 64, 32, [40, 70], [200, 70])])
+@pytest.mark.parametrize("scale", [0.0, -0.11, 3.0, 1e-30])
+def test_attention_scales(gpu, heads, kv, d, bs, new, lens, scale):
+    """Softmax scales of any sign; key and value blocks of zeros (scale 0); value scales far apart."""
+    P = Pool(7, heads, kv, d, bs, sum(-(-L // bs) for L in lens) + 2, "int8", "bf16")
+    P.codes[0, ::3], P.scale[0, ::3] = 0, 0
+    P.codes[1, 1::4], P.scale[1, 1::4] = 0, 0
+    P.scale[1, 2::5] *= np.float32(2.0 ** -40)
+    P.scale[1, 3::5] *= np.float32(2.0 ** 30)
+    run_attend(P, new, lens, True, "bf16", scale=scale)
+    P.codes[1], P.scale[1] = 0, 0                          # nothing but zeros
+    assert not run_attend(P, new, lens, True, "bf16", scale=scale).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("heads,kv,d,bs,new,lens", [
+    (4, 2, 128, 64, [1, 1], [300, 90]), (4, 4, 64, 16, [1] * 40, [100] * 40), (8, 2, 64, 16, [40, 70], [200, 300]), (2, 2, 128, 128, [200], [500])])
+def test_attention_leaves_bad_blocks_out(gpu, fmt, heads, kv, d, bs, new, lens):
+    P = Pool(3, heads, kv, d, bs, sum(-(-L // bs) for L in lens) + 2, fmt, "bf16")
+    table = make_table(P.rng, lens, bs, P.n, max(-(-L // bs) for L in lens) + 1, fill=-1)
+    table[0, 1], table[-1, 0] = P.n, -1                    # past the pool, negative
+    if lens[0] > 3 * bs:
+        table[0, 3], table[0, 2] = 2 ** 31 - 1, -2 ** 31
+    run_attend(P, new, lens, True, "bf16", table)
+    assert sv.get_status() == sv.ERR_INVALID_ARG and sv.get_status() == sv.OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,new", [(4, 2, 1), (4, 4, 30)])
+def test_attention_bounds_are_recorded(gpu, heads, kv, new):
+    """A length above max_len, more new tokens than max_new: cut and recorded; nothing outside is written."""
+    import torch
+    P = Pool(5, heads, kv, 64, 16, 12, "int8", "bf16")
+    c = P.to_device()
+    for lens, cu, max_new, max_len in (([60, 40], [0, new, 2 * new], new, 50), ([60, 40], [0, 2 * new + 3, 2 * new + 4], new, 64)):
+        b = sv.paged_batch(dev(np.arange(8, dtype=np.int32).reshape(2, 4)), dev(np.array(lens, np.int32)), dev(np.array(cu, np.int32)),
+                           n_tokens=2 * new + 4, max_new=max_new, max_len=max_len)
+        q = torch.ones(2 * new + 4, heads * 64, dtype=torch.bfloat16, device="cuda")
+        out = torch.full((2 * new + 6, heads * 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(max(16, sv.paged_attention_workspace_bytes(c, b)), dtype=torch.uint8, device="cuda")
+        sv.paged_attention(c, b, q, out[1:-1], ws)
+        assert sv.get_status() == sv.ERR_INVALID_ARG and sv.get_status() == sv.OK
+        assert (out[0] == 7).all() and (out[-1] == 7).all() and torch.isfinite(out.float()).all()
+
+
+class Server:
+    """A few steps of serving on the device and in the oracle: lengths, plan, append, attention."""
+
+    def __init__(self, seed, heads, kv, d, bs, B, max_blocks, n_blocks, max_new, fmt, dtype):
+        import torch
+        self.P = P = Pool(seed, heads, kv, d, bs, n_blocks, fmt, dtype)
+        self.B, self.max_new, self.dtype, self.cap = B, max_new, dtype, B * max_new
+        self.codes, self.scale = [P.codes[0], P.codes[1]], [P.scale[0], P.scale[1]]
+        self.table, self.ring, self.state = np.zeros((B, max_blocks), np.int32), np.arange(n_blocks, dtype=np.int32), (0, n_blocks)
+        i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+        self.c = P.to_device()
+        self.lens = [i32(B), i32(B)]
+        self.target, self.cu, self.slots, self.tab = i32(B), i32(B + 1), i32(self.cap), i32(B, max_blocks)
+        self.rng_dev, self.st = dev(self.ring), [dev(np.array([0, n_blocks, 0, 0], np.int32)), i32(4)]
+        row = (heads + 2 * kv) * d
+        self.x = torch.zeros(self.cap, row, dtype=dtype_of(dtype), device="cuda")
+        self.out = torch.zeros(self.cap, heads * d, dtype=dtype_of(dtype), device="cuda")
+        self.batches = [sv.paged_batch(self.tab, self.lens[k ^ 1], self.cu, self.slots, max_new=max_new, max_len=max_blocks * bs) for k in (0, 1)]
+        self.ws = torch.empty(max(16, sv.paged_attention_workspace_bytes(self.c, self.batches[0])), dtype=torch.uint8, device="cuda")
+        self.h = [0] * B
+        self.k = 0
+
+    def launch(self, k, stream=None):
+        P = self.P
+        q, kv = P.heads * P.d, P.kv * P.d
+        sv.paged_plan(self.batches[k], P.bs, self.lens[k], self.target, self.rng_dev, self.st[k], self.st[k ^ 1], stream=stream)
+        sv.paged_append(self.c, self.batches[k], self.x[:, q:q + kv], self.x[:, q + kv:], stream=stream)
+        sv.paged_attention(self.c, self.batches[k], self.x[:, :q], self.out, self.ws, stream=stream)
+
+    def step(self, target, run):
+        import torch
+        P, k = self.P, self.k
+        x = torch.from_numpy((P.rng.normal(size=tuple(self.x.shape)) * 2).astype(np.float32)).to(dtype_of(self.dtype))
+        self.x.copy_(x)
+        self.target.copy_(torch.tensor(target, dtype=torch.int32))
+        self.out.fill_(5.0)
+        torch.cuda.synchronize()
+        run(k)
+        torch.cuda.synchronize()
+        r = pk.plan(self.h, target, self.table, self.ring, *self.state, P.bs, self.cap, self.max_new, self.table.shape[1] * P.bs)
+        self.table, self.ring, self.h, self.state = r["table"], r["ring"], r["lens"].tolist(), (int(r["state"][0]), int(r["state"][1]))
+        n, x64 = int(r["cu"][-1]), x.double().numpy()
+        q, kv = P.heads * P.d, P.kv * P.d
+        for j in (0, 1):
+            self.codes[j], self.scale[j] = pk.append(x64[:n, q + j * kv:q + (j + 1) * kv].reshape(n, P.kv, P.d), r["slots"], r["cu"],
+                                                     self.codes[j], self.scale[j], P.fmt)
+            assert np.array_equal(P.t[2 * j].cpu().numpy(), self.codes[j]) and np.array_equal(P.t[2 * j + 1].cpu().numpy(), self.scale[j])
+        want, tol = pk.attend(x64[:n, :q].reshape(n, P.heads, P.d), r["cu"], self.h, self.table, self.codes[0], self.scale[0], self.codes[1],
+                              self.scale[1], P.fmt, True, P.d ** -0.5, UNIT[self.dtype])
+        got = self.out.double().cpu().numpy()
+        assert np.all(got[n:] == 5.0)
+        if n:
+            assert np.all(np.abs(got[:n].reshape(want.shape) - want) <= tol)
+        assert np.array_equal(self.st[k ^ 1].cpu().numpy(), r["state"])
+        self.k ^= 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,dtype,heads,kv,d,bs,B,max_blocks,n_blocks,max_new", [
+    ("int8", "bf16", 4, 2, 128, 16, 5, 8, 30, 40), ("e4m3", "fp16", 6, 3, 64, 32, 60, 4, 180, 1), ("e4m3", "bf16", 4, 4, 64, 64, 3, 20, 40, 500),
+    ("int8", "fp16", 8, 1, 128, 128, 2, 20, 30, 2)])
+@pytest.mark.parametrize("way", ["eager", "stream", "graph"])
+def test_serving_steps(gpu, fmt, dtype, heads, kv, d, bs, B, max_blocks, n_blocks, max_new, way):
+    """Plan, append and attention as a server runs them, call after call: eagerly, on another stream, and captured
+    once and replayed with other lengths (two graphs that share the workspace, one for each of the swapped lengths)."""
+    import torch
+    S = Server(B + max_new, heads, kv, d, bs, B, max_blocks, n_blocks, max_new, fmt, dtype)
+    run = S.launch
+    if way == "stream":
+        side = torch.cuda.Stream()
+        run = lambda k: S.launch(k, stream=side)  # noqa: E731
+    if way == "graph":
+        graphs = []
+        for k in (0, 1):                                   # captured with no work in it: the target is all zeros
+            S.launch(k)
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                S.launch(k)
+            graphs.append(g)
+        run = lambda k: graphs[k].replay()  # noqa: E731
+    r = random.Random(B)
+    for i in range(6):
+        target = []
+        for n in S.h:
+            u = r.random()
+            t = 0 if u < 0.15 else n if u < 0.25 else n + r.randint(1, max_new)
+            target.append(min(t, max_blocks * bs))
+        S.step(target, run)
+    assert sv.get_status() == sv.OK
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once(gpu):
+    """Two streams, each with its own workspace, over one cache."""
+    import torch
+    for heads, kv, new, lens in ((2, 1, [1], [9000]), (8, 4, [1] * 48, [500] * 48), (4, 2, [120, 300], [500, 2000])):
+        P = Pool(11, heads, kv, 128, 64, sum(-(-L // 64) for L in lens) + 1, "int8", "bf16")
+        c, n = P.to_device(), sum(new)
+        cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        b = sv.paged_batch(dev(make_table(P.rng, lens, 64, P.n, max(-(-L // 64) for L in lens))), dev(np.array(lens, np.int32)), dev(cu), n_tokens=n,
+                           max_new=max(new), max_len=max(lens))
+        q = [sixteen_bit(P.rng, (n, heads * 128), "bf16")[0] for _ in range(2)]
+        size = sv.paged_attention_workspace_bytes(c, b)
+        ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        want = [torch.empty_like(x) for x in q]
+        for x, o in zip(q, want):
+            sv.paged_attention(c, b, x, o, ws[0])
+        torch.cuda.synchronize()
+        streams, out = [torch.cuda.Stream() for _ in range(2)], [torch.zeros_like(x) for x in q]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for i in (0, 1):
+                sv.paged_attention(c, b, q[i], out[i], ws[i], stream=streams[i])
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, out))
+
+
+def test_calls_off_the_current_device_refused():
+    """Buffers that are not on the current CUDA device never reach a launch."""
+    import torch
+    z = lambda *s, t=torch.int32: torch.zeros(*s, dtype=t)  # noqa: E731
+    codes, scale = z(4 * 2 * 16 * 64, t=torch.uint8), z(8, t=torch.float32)
+    c = sv.paged_cache(4, 2, 64, 16, 4, "int8", "bf16", codes, scale, codes, scale)
+    b = sv.paged_batch(z(2, 2), z(2), z(3), z(4), max_new=2, max_len=32)
+    K, Q = z(4, 128, t=torch.bfloat16), z(4, 256, t=torch.bfloat16)
+    with pytest.raises(sv.SVDQError):
+        sv.paged_plan(b, 16, z(2), z(2), z(4), z(4), z(4))
+    with pytest.raises(sv.SVDQError):
+        sv.paged_append(c, b, K, K)
+    with pytest.raises(sv.SVDQError):
+        sv.paged_attention(c, b, Q, Q.clone(), z(1 << 20, t=torch.uint8))
+    with pytest.raises(sv.SVDQError):
+        sv.paged_batch(z(2, 2), z(2), z(3), max_new=2, max_len=32)   # neither slots nor n_tokens
