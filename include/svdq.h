@@ -234,8 +234,8 @@ svdq_status svdq_kv_attention(const void* Q, int32_t Mq, const uint8_t* kcodes, 
  * captured in a CUDA graph and replayed with other lengths.
  *
  * Limits: head_dim 64 or 128, block_size 16, 32, 64 or 128 (else
- * SVDQ_ERR_UNSUPPORTED); heads a multiple of kv_heads (heads h G .. h G + G - 1
- * read kv head h, G = heads / kv_heads); B <= 16384; n_blocks * block_size,
+ * SVDQ_ERR_UNSUPPORTED); heads <= 32768, a multiple of kv_heads (heads h G ..
+ * h G + G - 1 read kv head h, G = heads / kv_heads); B <= 16384; n_blocks * block_size,
  * B * max_blocks and max_blocks * block_size below 2^31.  Device pointers
  * 16-byte aligned unless said otherwise.
  */
@@ -308,7 +308,8 @@ svdq_status svdq_paged_plan(const svdq_paged_batch* b, int32_t block_size, int32
  * Slots: those of one request follow one another within a block, as the plan
  * writes them, and a block takes the new tokens of one request; a token whose
  * slot is -1, or not next to the previous one in its block, is left out.  A slot
- * past the pool is skipped and recorded for svdq_get_status (SVDQ_ERR_INVALID_ARG).
+ * past the pool is skipped, and more than max_new new tokens of a request may be
+ * left out; both are recorded for svdq_get_status (SVDQ_ERR_INVALID_ARG).
  * One kernel.  Errors: SVDQ_ERR_INVALID_ARG, SVDQ_ERR_ALIGNMENT,
  * SVDQ_ERR_UNSUPPORTED, SVDQ_ERR_CUDA.
  */
@@ -324,13 +325,15 @@ svdq_status svdq_paged_append(const svdq_paged_cache* c, const svdq_paged_batch*
  * see each other, and attention to an encoder's states (lens = the states' lengths,
  * cu of the queries) are causal = 0.  A row that sees nothing is 0.  Rows from
  * cu[B] on are not written; slots is not read (may be NULL).
- * Q: n_tokens rows of heads x head_dim, dtype; out: the same; strides in
- * elements, multiples of 8.  fp32 scores, maxima, sums and accumulators; weights
+ * Q: n_tokens rows of heads x head_dim, dtype; out: the same, apart from Q;
+ * strides in elements, multiples of 8.  fp32 scores, maxima, sums and accumulators; weights
  * are rounded to fp16 for the second product.  Results do not depend on timing.
  * A block number outside the pool is left out, a length above max_len or more
  * than max_new new tokens cut; each is recorded for svdq_get_status
  * (SVDQ_ERR_INVALID_ARG).  workspace: 16-byte aligned, >= the bytes below
- * (which depend on the host numbers alone), not shared by calls that may overlap.
+ * (which depend on the host numbers alone), not shared by calls that may overlap;
+ * nothing in it is kept from one call for the next.  One kernel, or two where the
+ * split of the work may cut a request.
  */
 size_t svdq_paged_attention_workspace_bytes(const svdq_paged_cache* c, const svdq_paged_batch* b);
 svdq_status svdq_paged_attention(const svdq_paged_cache* c, const svdq_paged_batch* b, const void* Q, int64_t q_stride,
