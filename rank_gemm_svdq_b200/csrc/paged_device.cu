@@ -270,7 +270,7 @@ struct AppendArgs {
 };
 
 template <int DT, int FMT, int D, int LB>
-__global__ void __launch_bounds__(append_threads(1 << LB, D)) paged_append_kernel(const AppendArgs A) {
+__global__ void __launch_bounds__(append_threads(1 << LB, D), 768 / append_threads(1 << LB, D)) paged_append_kernel(const AppendArgs A) {
   constexpr int kAppendThreads = append_threads(1 << LB, D);
   constexpr int BS = 1 << LB, kPerRow = D / 8, kRows = kAppendThreads / kPerRow, kPass = BS / kRows > 0 ? BS / kRows : 1;
   __shared__ float s_amax[kAppendThreads / 32];
