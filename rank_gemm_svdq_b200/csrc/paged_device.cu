@@ -486,29 +486,35 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 16 rows of queries as normalised fp16 in shared memory (row pitch D + 8) and
-// each row's factor 2^e scale log2(e).  Rows past the request's are zero.
-template <int DT, int D>
-__device__ __forceinline__ void load_queries(const AttnArgs& A, const Rows& R, int h, int r0, int nrows, __half* sq,
-                                             float* sf, int warp, int nwarps, int lane) {
-  for (int rr = warp; rr < nrows; rr += nwarps) {
-    const int r = r0 + rr;
-    float v[D / 32], top = 0.0f;
+// NR rows of queries as normalised fp16 in shared memory (row pitch D + 8) and each
+// row's factor 2^e |scale| log2(e), by W warps.  Rows past the request's are zero.
+template <int DT, int D, int NR, int W>
+__device__ __forceinline__ void load_queries(const AttnArgs& A, const Rows& R, int h, __half* sq, float* sf, int warp, int lane) {
+  static_assert(NR % (2 * W) == 0, "rows in pairs");
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) v[k] = 0.0f;
-    if (r < R.rows) {
-      const uint16_t* q = A.q + (int64_t)(R.a + r / A.G) * A.q_stride + (int64_t)(h * A.G + r % A.G) * D;
+  for (int i0 = 0; i0 < NR / W; i0 += 2) {
+    uint2 w[2];
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) { v[k] = load16<DT>(q[lane + 32 * k]); top = fmaxf(top, fabsf(v[k])); }
+    for (int i = 0; i < 2; ++i) {
+      const int r = warp + (i0 + i) * W;
+      w[i] = make_uint2(0, 0);
+      if (r < R.rows && lane < D / 4)
+        w[i] = *reinterpret_cast<const uint2*>(A.q + (int64_t)(R.a + r / A.G) * A.q_stride + (int64_t)(h * A.G + r % A.G) * D + 4 * lane);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int e = clampi((int)(__float_as_uint(top) >> 23) - 127, -100, 100);
-    // the factor is kept non-negative (maxima are taken before it): a negative scale turns the query instead
-    const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), A.scale_log2);
+    for (int i = 0; i < 2; ++i) {
+      const int r = warp + (i0 + i) * W;
+      const float v0 = load16<DT>((uint16_t)w[i].x), v1 = load16<DT>((uint16_t)(w[i].x >> 16));
+      const float v2 = load16<DT>((uint16_t)w[i].y), v3 = load16<DT>((uint16_t)(w[i].y >> 16));
+      float top = fmaxf(fmaxf(fabsf(v0), fabsf(v1)), fmaxf(fabsf(v2), fabsf(v3)));
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) sq[rr * (D + 8) + lane + 32 * k] = __float2half_rn(v[k] * down);
-    if (lane == 0) sf[rr] = __uint_as_float((uint32_t)(127 + e) << 23) * fabsf(A.scale_log2);
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = clampi((int)(__float_as_uint(top) >> 23) - 127, -100, 100);
+      // the factor is kept non-negative (maxima are taken before it): a negative scale turns the query instead
+      const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), A.scale_log2);
+      if (lane < D / 4) *reinterpret_cast<uint2*>(sq + r * (D + 8) + 4 * lane) = make_uint2(pack_half2(v0 * down, v1 * down), pack_half2(v2 * down, v3 * down));
+      if (lane == 0) sf[r] = __uint_as_float((uint32_t)(127 + e) << 23) * fabsf(A.scale_log2);
+    }
   }
 }
 
@@ -523,7 +529,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs& A, const Rows& R, i
 // schedule (paged_flat_kernel).  The fragments are read straight from the codes: the order of the
 // contraction over d is free, so 16 bytes of a key row serve 4 k-steps, and 16 bytes
 // of four value rows the 16 values of d that a lane needs.
-constexpr int kDecWarps = 4, kDecTile = 32, kDecStages = 2, kDecGroup = 16, kMaxCluster = 8;
+constexpr int kDecWarps = 4, kDecTile = 32, kDecStages = 2, kDecGroup = 32, kMaxCluster = 8;
 constexpr int dec_stage_bytes(int D) { return kDecTile * D * 2; }
 constexpr int dec_ring_bytes(int D) { return kDecWarps * kDecStages * dec_stage_bytes(D); }
 struct DecMeta { float sk[2], sv[2]; };
@@ -834,7 +840,7 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
   };
   for (int k = 0; k < min(mine, NST); ++k) issue(k);
 
-  load_queries<DT, D>(A, R, h, 0, NR, sq, sf, warp, kDecWarps, lane);
+  load_queries<DT, D, NR, kDecWarps>(A, R, h, sq, sf, warp, lane);
   __syncthreads();
   RowState<FMT, D, NB> S;
   S.start(A, R, sq, sf, t_end, lane);
@@ -1075,8 +1081,10 @@ struct Walk {
 template <int D, int NB>
 struct FlatSmem {
   uint8_t ring[dec_ring_bytes(D)];
-  float sum[8 * NB][D];
-  __half q[8 * NB][D + 8];
+  union {
+    float sum[8 * NB][D + 4];                              // value d = (D / 8) g + 2 j + e at 2 (8 j + g) + e
+    __half q[8 * NB][D + 8];
+  };
   DecMeta meta[kDecWarps][2 * kDecGroup];
   int2 ids[kDecWarps][2 * kDecGroup];
   float2 ml[kDecWarps][8 * NB];
@@ -1116,6 +1124,7 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_flat_kernel(const AttnAr
   // the tiles on their way: `sent` so far, the next one at token `t` of the item below `t_end`
   Walk ahead;
   ahead.start(A, share, NR);
+  Walk walk = ahead;
   int sent = 0, t = 0, t_end = 0, h = 0, grouped = 0;
   const int* row = nullptr;
   const auto send = [&]() {
@@ -1172,8 +1181,6 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_flat_kernel(const AttnAr
   };
   for (int s = 0; s < NST; ++s) send();
 
-  Walk walk;
-  walk.start(A, share, NR);
   Item I;
   int done = 0;
   bool dead = false;
@@ -1181,7 +1188,8 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_flat_kernel(const AttnAr
   while (walk.next(A, share, NR, I)) {
     const Rows R = {I.a, I.n, I.L, I.rows};
     const int end = end_of(I);
-    load_queries<DT, D>(A, R, I.h, 0, NR, &X.q[0][0], X.f, warp, kDecWarps, lane);
+    __syncthreads();                                       // the sums of the item before are read
+    load_queries<DT, D, NR, kDecWarps>(A, R, I.h, &X.q[0][0], X.f, warp, lane);
     __syncthreads();
     S.start(A, R, &X.q[0][0], X.f, end, lane);
     for (int at = I.lo * kTileTok + 32 * warp; at < end && !dead; at += kTileTok, ++done) {
@@ -1212,11 +1220,12 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_flat_kernel(const AttnAr
           for (int i = 0; i < 2; ++i) {
             const int r = nb * 8 + 2 * (lane & 3) + i;
             const float wt = weight(w, r, top(r)) * X.vref[w];
-            float2* p = reinterpret_cast<float2*>(&X.sum[r][(D / 8) * (lane >> 2)]);
+            // rows 16 bytes and lanes 8 bytes apart: no two lanes of a half warp on one bank
+            float2* p = reinterpret_cast<float2*>(&X.sum[r][2 * (lane >> 2)]);
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
-              const float2 v = w == 0 ? make_float2(0.0f, 0.0f) : p[j];
-              p[j] = make_float2(v.x + S.o[j][nb][i] * wt, v.y + S.o[j][nb][i + 2] * wt);
+              const float2 v = w == 0 ? make_float2(0.0f, 0.0f) : p[8 * j];
+              p[8 * j] = make_float2(v.x + S.o[j][nb][i] * wt, v.y + S.o[j][nb][i + 2] * wt);
             }
           }
       }
@@ -1231,7 +1240,9 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_flat_kernel(const AttnAr
       float L = 0.0f;
 #pragma unroll
       for (int w = 0; w < kDecWarps; ++w) L += weight(w, r, M) * X.ml[w][r].y;
-      const float4 v = *reinterpret_cast<const float4*>(&X.sum[r][d]);
+      const int at = 2 * (4 * (d % (D / 8)) + d / (D / 8));
+      const float2 v0 = *reinterpret_cast<const float2*>(&X.sum[r][at]), v1 = *reinterpret_cast<const float2*>(&X.sum[r][at + 16]);
+      const float4 v = make_float4(v0.x, v0.y, v1.x, v1.y);
       if (I.out == kItemWhole) {
         const int token = R.a + r / A.G, head = I.h * A.G + r % A.G;
         store_row4<DT>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + d, v, L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f);
