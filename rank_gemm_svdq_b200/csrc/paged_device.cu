@@ -2058,10 +2058,10 @@ Split split_of(const svdq_paged_cache* c, const svdq_paged_batch* b) {
     return Split{kTileRows, within(items * tiles, kSplitSms), 0, 0};
   }
   const int nr = rows <= 8 ? 8 : 16;
-  const int64_t want = std::min((4 * kSplitSms + cells - 1) / cells, (len + 255) / 256);
-  if (cells < kSplitSms && want <= kMaxCluster) return Split{nr, want > 4 ? 8 : want > 2 ? 4 : (int)want, 1, 0};
+  const int64_t room = (int64_t)kSplitSms * flat_per_sm(c->head_dim, nr), want = std::min(room / cells, (len + 255) / 256);
+  if (cells < kSplitSms && want <= kMaxCluster) return Split{nr, want >= 8 ? 8 : want >= 4 ? 4 : want >= 2 ? 2 : 1, 1, 0};
   // whole items where they are short: a cut costs a second kernel, an uneven share at most two tiles
-  return Split{nr, within(cells * tiles, (int64_t)kSplitSms * flat_per_sm(c->head_dim, nr)), 0, tiles <= 2};
+  return Split{nr, within(cells * tiles, room), 0, tiles <= 2};
 }
 bool joins(const Split& s) { return !s.cluster && !s.snap && s.ctas > 1; }
 
