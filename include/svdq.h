@@ -236,7 +236,8 @@ svdq_status svdq_kv_attention(const void* Q, int32_t Mq, const uint8_t* kcodes, 
  * Limits: head_dim 64 or 128, block_size 16, 32, 64 or 128 (else
  * SVDQ_ERR_UNSUPPORTED); heads <= 32768, a multiple of kv_heads (heads h G ..
  * h G + G - 1 read kv head h, G = heads / kv_heads); B <= 16384; n_blocks * block_size,
- * B * max_blocks and max_blocks * block_size below 2^31.  Device pointers
+ * B * max_blocks and max_blocks * block_size below 2^31; n_tokens, max_len and
+ * max_new * G at most 2^31 - 65537 (else SVDQ_ERR_UNSUPPORTED).  Device pointers
  * 16-byte aligned unless said otherwise.
  */
 typedef enum { SVDQ_KV_INT8 = 1, SVDQ_KV_E4M3 = 2 } svdq_kv_format;

@@ -27,6 +27,8 @@ namespace paged {
 using namespace svdq::dev;
 
 constexpr int kMaxRequests = 16384;
+// Tokens, lengths and rows stay this far from 2^31: the kernels round them up to tiles in 32 bits.
+constexpr int kMaxCount = INT32_MAX - 65536;
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
@@ -1302,6 +1304,8 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // 2^d for a whole number d <= 0 (0 below the normal numbers).
 __device__ __forceinline__ float power_of_two(float d) { return __uint_as_float((uint32_t)(max((int)d, -127) + 127) << 23); }
 
@@ -1471,6 +1475,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
     if (some) queries(items[0]);
     while (some) {
       const Item& I = items[k % kItems];
+      if (mbar_try_wait(&i_full[(k + 1) % kItems], ((k + 1) / kItems) & 1)) {   // the next item's queries, to L2
+        const Item& N = items[(k + 1) % kItems];
+        const int r = N.r0 + rt * 128 + rl;
+        if (N.hi >= 0 && r < N.rows) {
+          const uint16_t* row = A.q + (int64_t)(N.a + r / A.G) * A.q_stride + (int64_t)(N.h * A.G + r % A.G) * D;
+          prefetch_l2(row);
+          if (D == 128) prefetch_l2(row + 64);
+        }
+        __syncwarp();
+      }
       const int lo = I.lo, end = I.end[rt], rows = I.rows - (I.r0 + rt * 128);   // rows of this row tile
       int see = INT_MAX, clear;
       {
@@ -1980,6 +1994,7 @@ svdq_status check_batch(const svdq_paged_batch* b, int bs) {
   if (b->B < 1 || b->B > kMaxRequests || b->max_blocks < 1 || b->n_tokens < 0 || b->max_new < 1 || b->max_len < 0)
     return SVDQ_ERR_INVALID_ARG;
   if ((int64_t)b->B * b->max_blocks > INT32_MAX || (int64_t)b->max_blocks * bs > INT32_MAX) return SVDQ_ERR_UNSUPPORTED;
+  if (b->n_tokens > kMaxCount || b->max_len > kMaxCount) return SVDQ_ERR_UNSUPPORTED;
   if ((int64_t)b->max_len > (int64_t)b->max_blocks * bs) return SVDQ_ERR_INVALID_ARG;
   return SVDQ_OK;
 }
@@ -2234,6 +2249,7 @@ svdq_status svdq_paged_append(const svdq_paged_cache* c, const svdq_paged_batch*
 
 size_t svdq_paged_attention_workspace_bytes(const svdq_paged_cache* c, const svdq_paged_batch* b) {
   if (check_cache(c) != SVDQ_OK || check_batch(b, c->block_size) != SVDQ_OK) return 0;
+  if ((int64_t)b->max_new * (c->heads / c->kv_heads) > kMaxCount) return 0;
   return attention_ws(c, b);
 }
 
@@ -2246,6 +2262,7 @@ svdq_status svdq_paged_attention(const svdq_paged_cache* c, const svdq_paged_bat
   if (b->n_tokens == 0) return SVDQ_OK;
   if (!Q || !out || !workspace || !b->cu || !b->lens || !b->table || (causal != 0 && causal != 1) || !std::isfinite(scale))
     return SVDQ_ERR_INVALID_ARG;
+  if ((int64_t)b->max_new * (c->heads / c->kv_heads) > kMaxCount) return SVDQ_ERR_UNSUPPORTED;
   const int64_t row = (int64_t)c->heads * c->head_dim;
   if (q_stride < row || out_stride < row) return SVDQ_ERR_INVALID_ARG;
   if (ws_bytes < attention_ws(c, b)) return SVDQ_ERR_WORKSPACE;

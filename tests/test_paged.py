@@ -654,3 +654,26 @@ def test_calls_off_the_current_device_refused():
         sv.paged_attention(c, b, Q, Q.clone(), z(1 << 20, t=torch.uint8))
     with pytest.raises(sv.SVDQError):
         sv.paged_batch(z(2, 2), z(2), z(3), max_new=2, max_len=32)   # neither slots nor n_tokens
+
+
+def test_counts_near_2_31_refused():
+    c, big = raw_cache(), 2 ** 31 - 65536
+    for bad in (dict(n_tokens=big), dict(max_len=big, max_blocks=(2 ** 31 - 1) // 16, B=1)):
+        b = raw_batch(**bad)
+        assert call_append(c, b) == call_attend(c, b) == call_plan(raw_batch(lens=12288, **bad)) == sv.ERR_UNSUPPORTED
+    b = raw_batch(max_new=2 ** 30)                         # two query heads a key head: 2^31 rows a request
+    assert call_attend(c, b) == sv.ERR_UNSUPPORTED and sv.lib().svdq_paged_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(b)) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("max_len,new", [(0, [1, 0, 1]), (40, [2, 3, 40])])
+def test_attention_over_empty_caches(gpu, max_len, new):
+    """Requests without a cached token, and more new tokens than cached ones: rows that see nothing are 0."""
+    for B in (1, 60):
+        P = Pool(2, 4, 4, 64, 16, 4, "int8", "bf16")
+        lens = [0, min(max_len, 17), 0] * B
+        table = np.zeros((3 * B, 4), np.int32)
+        table[1::3, :2] = (1, 3)
+        run_attend(P, new * B, lens, True, "bf16", table, max_len=max_len)
+        run_attend(P, new * B, lens, False, "bf16", table, max_len=max_len)
+    assert sv.get_status() == sv.OK
