@@ -289,8 +289,9 @@ typedef struct svdq_paged_batch {
  * same result.  Blocks given back are available to the next call.
  * Refused as a whole, when the ring lacks blocks (lacking = how many) or the
  * lengths are bad (lacking = -1: negative, above max_len, more than max_new new
- * for one request or n_tokens for all, head or count outside the ring): no
- * block moves, b->lens = prev, b->cu = 0, b->slots = -1.
+ * for one request or n_tokens for all, head or count outside the ring, count and
+ * the blocks given back together above n_blocks): no block moves, b->lens = prev,
+ * b->cu = 0, b->slots = -1.
  * One kernel.  Errors: SVDQ_ERR_INVALID_ARG, SVDQ_ERR_UNSUPPORTED, SVDQ_ERR_CUDA.
  */
 svdq_status svdq_paged_plan(const svdq_paged_batch* b, int32_t block_size, int32_t n_blocks, const int32_t* prev,

@@ -65,7 +65,7 @@ def plan(prev, target, table, ring, head, count, bs, n_tokens, max_new, max_len)
     if not bad:
         take = sum(max(0, blocks(t) - blocks(p)) for p, t in zip(prev, target))
         give = sum(max(0, blocks(p) - blocks(t)) for p, t in zip(prev, target))
-        lacking = -1 if count - take + give > n else max(0, take - count)
+        lacking = -1 if count + give > n else max(0, take - count)
     slots = np.full(n_tokens, -1, np.int32)
     if lacking != 0:
         return dict(table=table, lens=np.array(prev, np.int32), cu=np.zeros(len(prev) + 1, np.int32), slots=slots,

@@ -131,7 +131,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
   if (bad) s_bad = 1;
   if (tid == 0) { s_new[A.B] = (int)c_new; s_take[A.B] = c_take; s_give[A.B] = c_give; }
   __syncthreads();
-  const bool wrong = s_bad != 0 || c_new > A.n_tokens || (int64_t)count - c_take + c_give > A.n_blocks;
+  // entries given back are written from head + count on: they must not reach those being taken
+  const bool wrong = s_bad != 0 || c_new > A.n_tokens || (int64_t)count + c_give > A.n_blocks;
   const int lacking = wrong ? -1 : (c_take > count ? c_take - count : 0);
   const bool ok = lacking == 0;
   const int gtid = blockIdx.x * kPlanThreads + tid, stride = gridDim.x * kPlanThreads;
