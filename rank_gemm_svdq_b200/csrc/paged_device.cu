@@ -398,8 +398,8 @@ __global__ void __launch_bounds__(append_threads(1 << LB, D), 768 / append_threa
 // ----------------------------------------------------------------- attention
 // Row r of request i, kv head h: new token r / G, query head h G + r % G.  With
 // codes c and scales s per block: x_t = scale 2^e s_k (q' . c_t) log2(e), where
-// q' = q 2^-e in fp16 (e: exponent of the row's largest entry, so q' is exact up to
-// 2^-25 of that entry); out = sum_t p_t s_v c^v_t / sum_t p_t, p_t = 2^(x_t - m).
+// q' = q 2^-e in fp16 (e: exponent of the row's largest entry, within [-120, 113], so q' is
+// exact up to 2^-25 of that entry, of 2^-120 for smaller ones); out = sum_t p_t s_v c^v_t / sum_t p_t, p_t = 2^(x_t - m).
 // Both products run on fp16 operands (8-bit codes are exact in fp16) with fp32
 // accumulators.  The value scale is folded into p before it is rounded to fp16,
 // relative to a value scale seen so far, as m is a score seen so far: both may lag by
@@ -487,6 +487,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The exponent e that a row of queries is divided by, from its largest magnitude.  Its limits leave every finite bf16
+// query at most 2^15 after the division (an fp16 number) and 2^e scale within fp32; rows below 2^-120 keep
+// what fp16 has of them after that much.
+__device__ __forceinline__ int query_exponent(float top) { return clampi((int)(__float_as_uint(top) >> 23) - 127, -120, 113); }
+
 constexpr float kGrow = 7.0f, kGrowFactor = 128.0f;   // a softmax reference may lag by this much (2^7)
 
 __device__ __forceinline__ float ex2(float x) {
@@ -518,7 +523,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs& A, const Rows& R, i
       float top = fmaxf(fmaxf(fabsf(v0), fabsf(v1)), fmaxf(fabsf(v2), fabsf(v3)));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = clampi((int)(__float_as_uint(top) >> 23) - 127, -100, 100);
+      const int e = query_exponent(top);
       // the factor is kept non-negative (maxima are taken before it): a negative scale turns the query instead
       const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), A.scale_log2);
       if (lane < D / 4) *reinterpret_cast<uint2*>(sq + r * (D + 8) + 4 * lane) = make_uint2(pack_half2(v0 * down, v1 * down), pack_half2(v2 * down, v3 * down));
@@ -1450,7 +1455,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
 #pragma unroll
         for (int o = PER / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int e = clampi((int)(__float_as_uint(top) >> 23) - 127, -100, 100);
+        const int e = query_exponent(top);
         // the factor is kept non-negative (maxima are taken before it): a negative scale turns the query instead
         const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), A.scale_log2);
         *reinterpret_cast<uint4*>(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) =

@@ -7,7 +7,57 @@ import pytest
 
 import rank_gemm_svdq_b200 as sv
 from oracle import pagedkv as pk
-from tests.test_paged import dev
+from tests.test_paged import UNIT, Pool, dev, dtype_of, make_table
+
+
+def both(P, q, new, lens, table, causal=True, dtype="bf16", scale=None, max_new=None):
+    """Attention of q (tokens x heads d, 16-bit values held in float32) over the pool, by the kernels and the oracle:
+    the 16-bit result, its values, the oracle's and how far a value may be off."""
+    import torch
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    n = int(cu[-1])
+    want, tol = pk.attend(q.double().numpy().reshape(n, P.heads, P.d), cu, lens, table, P.codes[0], P.scale[0], P.codes[1], P.scale[1],
+                          P.fmt, causal, P.d ** -0.5 if scale is None else scale, UNIT[dtype])
+    c = P.to_device()
+    b = sv.paged_batch(dev(table), dev(np.array(lens, np.int32)), dev(cu), None, n_tokens=n, max_new=max_new or max(new), max_len=max(lens))
+    ws = torch.full((sv.paged_attention_workspace_bytes(c, b),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.full((n, P.heads * P.d), 7.0, dtype=dtype_of(dtype), device="cuda")
+    sv.paged_attention(c, b, q.to(dtype_of(dtype)).cuda(), out, ws, causal=causal, scale=scale)
+    return out.cpu(), out.double().cpu().numpy().reshape(n, P.heads, P.d), want, tol
+
+
+def normal(rng, n, cols, dtype="bf16", power=0):
+    """Random 16-bit values times a power of two."""
+    import torch
+    x = torch.from_numpy(rng.normal(size=(n, cols)).astype(np.float32)).to(dtype_of(dtype)).float() * 2.0 ** power
+    return x.to(dtype_of(dtype)).float()
+
+
+def within(got, want, tol):
+    assert np.isfinite(got).all()
+    off = np.abs(got - want) - tol
+    assert off.max() <= 0, (off.max(), np.unravel_index(np.argmax(off), off.shape))
+
+
+# A shape for each kernel and each way of sharing the work out: heads, kv, d, bs, new, lens.  The last block of every
+# request holds a few tokens of its own, so that some of its new rows do not see that block.
+PATHS = [
+    (4, 4, 64, 16, [8], [101]),                            # a CTA a cell
+    (4, 2, 128, 16, [4, 3], [2003, 402]),                  # clusters
+    (8, 2, 64, 32, [3], [514]),                            # clusters, 9 to 16 rows
+    (2, 2, 128, 32, [7], [8996]),                          # one long request over the whole chip, cut and joined
+    (8, 1, 64, 64, [2], [6017]),                           # the same, 9 to 16 rows
+    (4, 4, 64, 16, [6] * 45, [85 + 16 * (i % 40) for i in range(45)]),   # many cells: shares cut inside requests
+    (16, 4, 128, 64, [4] * 50, [66] * 50),                 # 16 rows, whole items
+    (2, 1, 64, 16, [40, 33], [101, 340]),                  # tensor-core rows
+    (4, 2, 128, 64, [300], [1064]),                        # the same, cut and joined
+]
+BOTH_FORMATS = [("int8", "bf16"), ("e4m3", "fp16")]
+
+
+def pool(seed, heads, kv, d, bs, lens, fmt, dtype):
+    P = Pool(seed, heads, kv, d, bs, sum(-(-L // bs) for L in lens) + 2, fmt, dtype)
+    return P, make_table(P.rng, lens, bs, P.n, max(-(-L // bs) for L in lens) + 1, fill=-1)
 
 
 # -------------------------------------------- the plan: what is given back has to fit the ring
@@ -54,3 +104,16 @@ def test_plan_refuses_more_blocks_than_the_ring_has_room_for(gpu):
     for name in t:
         assert np.array_equal(t[name].cpu().numpy(), want[name]), name
     assert np.array_equal(out.cpu().numpy(), want["state"])
+
+
+# ---------------------------------------------------- the smallest and the largest numbers
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("power", [125, 116, 100, -100, -120])
+def test_queries_of_extreme_size(gpu, heads, kv, d, bs, new, lens, fmt, power):
+    """Queries near 2^power over keys near 2^-power: the scores are ordinary ones."""
+    P, table = pool(sum(lens) + 3, heads, kv, d, bs, lens, fmt, "bf16")
+    P.scale[0] = (P.scale[0].astype(np.float64) * 2.0 ** (-power if power > 0 else min(-power, 112))).astype(np.float32)
+    _, got, want, tol = both(P, normal(P.rng, sum(new), heads * d, power=power), new, lens, table)
+    within(got, want, tol)
