@@ -329,7 +329,9 @@ svdq_status svdq_paged_append(const svdq_paged_cache* c, const svdq_paged_batch*
  * cu[B] on are not written; slots is not read (may be NULL).
  * Q: n_tokens rows of heads x head_dim, dtype; out: the same, apart from Q;
  * strides in elements, multiples of 8.  fp32 scores, maxima, sums and accumulators; weights
- * are rounded to fp16 for the second product.  Results do not depend on timing.
+ * are rounded to fp16 for the second product, value scale included (2^-11 of the weight, or
+ * 2^-24 of the largest weight times scale that the row sees).  A row's result depends on
+ * the blocks that it sees alone, and not on timing.
  * A block number outside the pool is left out, a length above max_len or more
  * than max_new new tokens cut; each is recorded for svdq_get_status
  * (SVDQ_ERR_INVALID_ARG).  workspace: 16-byte aligned, >= the bytes below

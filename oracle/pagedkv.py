@@ -20,6 +20,7 @@ import numpy as np
 
 F32 = np.float32
 QMAX = {"int8": F32(127.0), "e4m3": F32(448.0)}
+NORMAL = {2.0 ** -8: 2.0 ** -126, 2.0 ** -11: 2.0 ** -14}   # smallest normal number by half a step: bf16, fp16
 
 
 def e4m3_values() -> np.ndarray:
@@ -133,10 +134,15 @@ def gather(codes, scale, row, length, fmt):
 def attend(q, cu, lens, table, kcodes, kscale, vcodes, vscale, fmt, causal, scale, unit=2.0 ** -8):
     """q: tokens x heads x d (float64 holding 16-bit values).  Returns (out, tol): the float64 result and, per
     value, how far a kernel may be off that rounds the weights to fp16 and the result to a type of half step `unit`:
-      unit |out|                      the result's own rounding
+      unit max(|out|, N)              the result's own rounding, N the type's smallest normal number
       (2^-11 + 2 dx + 2^-19) E        weights to fp16; an error dx of a score moves a weight, and the sum of the
                                       weights, by that share; exponentials and sums to 2^-20 each.  E = sum p |v|
-      T 2^-25 max s_v qmax            weights that fall below fp16's normal numbers, of T tokens
+      2^-23 (2 |log2 s_v| + |x|) E    the roundings of an exponent x + log2 s_v and of its terms (largest of each)
+      T qmax F                        what is lost below fp16's normal numbers, half a step of 2^-24 for each of the T
+                                      tokens that the row sees.  The step belongs to weights p s_v taken relative to a
+                                      reference at most twice the largest one that the row sees, so F = 2^-24 max p s_v;
+                                      2^-144 max p more where all s_v are below 2^-120 (the reference's lower end);
+                                      2^-119 max p max s_v for weights below the smallest fp32 number
     with dx = (d 2^-23) scale max_t sum |q| |k|: fp32 products added in any order, and q's own 2^-25."""
     n, heads, d = q.shape
     kv = kcodes.shape[1]
@@ -148,10 +154,9 @@ def attend(q, cu, lens, table, kcodes, kscale, vcodes, vscale, fmt, causal, scal
             continue
         K, V = gather(kcodes, kscale, table[i], L, fmt), gather(vcodes, vscale, table[i], L, fmt)
         there = ~np.isnan(K[0, :, 0])
-        used = [int(b) for b in table[i][:-(-L // kcodes.shape[2])] if 0 <= int(b) < kcodes.shape[0]]
+        blocks = np.repeat(table[i][:-(-L // kcodes.shape[2])].astype(np.int64), kcodes.shape[2])[:L]
         for h in range(heads):
             k, v = np.nan_to_num(K[h // G]), np.nan_to_num(V[h // G])
-            floor = L * 2.0 ** -25 * float(max([vscale[b, h // G] for b in used], default=0)) * float(QMAX[fmt])
             s = q[a:e, h] @ k.T * scale
             seen = np.broadcast_to(there, s.shape).copy()
             if causal:
@@ -162,5 +167,11 @@ def attend(q, cu, lens, table, kcodes, kscale, vcodes, vscale, fmt, causal, scal
             p /= np.maximum(p.sum(axis=1, keepdims=True), 1e-300)
             out[a:e, h] = p @ v
             dx = d * 2.0 ** -23 * abs(scale) * (np.abs(q[a:e, h]) @ np.abs(k).T).max(axis=1, keepdims=True)
-            tol[a:e, h] = unit * np.abs(out[a:e, h]) + (2.0 ** -11 + 2 * dx + 2.0 ** -19) * (p @ np.abs(v)) + floor
+            sv = np.where(there, vscale[np.where(there, blocks, 0), h // G].astype(np.float64), 0.0)
+            most = lambda w: np.max(np.where(seen, w, 0.0), axis=1, keepdims=True)  # noqa: E731
+            lost = 2.0 ** -24 * most(p * sv) + 2.0 ** -144 * most(p) + 2.0 ** -119 * most(p) * most(sv)
+            far = 2 * most(np.abs(np.log2(np.where(sv > 0, sv, 1.0)))) + 1.45 * most(np.where(seen, np.abs(s), 0.0))
+            tol[a:e, h] = unit * np.maximum(np.abs(out[a:e, h]), NORMAL[unit])
+            tol[a:e, h] += (2.0 ** -11 + 2 * dx + 2.0 ** -19 + 2.0 ** -23 * far) * (p @ np.abs(v))
+            tol[a:e, h] += seen.sum(axis=1, keepdims=True) * float(QMAX[fmt]) * lost
     return out, tol

@@ -401,10 +401,15 @@ __global__ void __launch_bounds__(append_threads(1 << LB, D), 768 / append_threa
 // q' = q 2^-e in fp16 (e: exponent of the row's largest entry, within [-120, 113], so q' is
 // exact up to 2^-25 of that entry, of 2^-120 for smaller ones); out = sum_t p_t s_v c^v_t / sum_t p_t, p_t = 2^(x_t - m).
 // Both products run on fp16 operands (8-bit codes are exact in fp16) with fp32
-// accumulators.  The value scale is folded into p before it is rounded to fp16,
-// relative to a value scale seen so far, as m is a score seen so far: both may lag by
-// 2^kGrow, so p' <= 2^14 does not overflow (one rounding of 2^-11 per weight, the size
-// of the rounding of an fp16 output), and what was summed is rarely rescaled.
+// accumulators.  The sum takes p relative to m, a score seen so far; the product takes
+// p' = p s_v = 2^(x + log2 s_v - n), rounded to fp16, relative to n, a weighted
+// magnitude x + log2 s_v seen so far.  Both come from what the row sees alone, so that
+// a large scale behind a causal mask, or of no weight, costs nothing.  Both may lag by 2^kGrow:
+// p' <= 2^7 does not overflow, what was summed is rarely rescaled, and a weight is
+// off by 2^-11 of itself (the size of the rounding of an fp16 output) or, below fp16's
+// normal numbers, by 2^-24 of the row's largest weighted magnitude.  At the end
+// O 2^(n - m) / l; pieces of rows are kept so divided and joined as means with the weights
+// 2^m l, which no sum of large values overflows.
 struct AttnArgs {
   const uint16_t* q;
   uint16_t* out;
@@ -492,12 +497,24 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // what fp16 has of them after that much.
 __device__ __forceinline__ int query_exponent(float top) { return clampi((int)(__float_as_uint(top) >> 23) - 127, -120, 113); }
 
-constexpr float kGrow = 7.0f, kGrowFactor = 128.0f;   // a softmax reference may lag by this much (2^7)
+constexpr float kGrow = 7.0f;   // a softmax reference may lag by this much (2^7)
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// At least log2 s, at most one more; -120 for smaller s (so that 2^(m - n) is an fp32 number).
+__device__ __forceinline__ float scale_exponent(float s) {
+  return fmaxf(__uint_as_float(0x4B000000u | (__float_as_uint(s) >> 23)) - 8388734.0f, -120.0f);   // 2^23 + field - (2^23 + 126)
+}
+
+// A row's accumulator in units of 2^n to its result, 2^(n - m) / l, as two factors that neither over- nor underflow.
+__device__ __forceinline__ float2 result_factors(float n, float m, float l) {
+  if (!(l > 0.0f)) return make_float2(0.0f, 0.0f);         // a row that sees nothing
+  const float g = ex2(0.5f * (n - m));
+  return make_float2(g, __fdiv_rn(g, l));
 }
 
 // NR rows of queries as normalised fp16 in shared memory (row pitch D + 8) and each
@@ -565,10 +582,10 @@ __device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
 }
 
 template <int DT>
-__device__ __forceinline__ void store_row4(uint16_t* dst, const float4& v, float mul) {
+__device__ __forceinline__ void store_row4(uint16_t* dst, const float4& v) {
   uint2 w;
-  w.x = (uint32_t)store16<DT>(v.x * mul) | ((uint32_t)store16<DT>(v.y * mul) << 16);
-  w.y = (uint32_t)store16<DT>(v.z * mul) | ((uint32_t)store16<DT>(v.w * mul) << 16);
+  w.x = (uint32_t)store16<DT>(v.x) | ((uint32_t)store16<DT>(v.y) << 16);
+  w.y = (uint32_t)store16<DT>(v.z) | ((uint32_t)store16<DT>(v.w) << 16);
   *reinterpret_cast<uint2*>(dst) = w;
 }
 
@@ -589,13 +606,12 @@ template <int FMT, int D, int NB>
 struct RowState {
   static constexpr int KC = D / 64, VW = D / 32;
   uint32_t qf[NB][D / 16][2];
-  float f[NB][2], o[D / 16][NB][4], m[NB][2], l[NB][2], vref, rv;   // rv = 1 / vref
+  float f[NB][2], o[D / 16][NB][4], m[NB][2], l[NB][2], n[NB][2];
   int see[NB][2], clear, last;                                   // clear: tiles that end at or below it need no mask
 
   // Q^T fragments: k-step s covers d = 64 (s / 4) + 16 q4 + 4 (s % 4) + {0, 1 | 2, 3}
   __device__ __forceinline__ void start(const AttnArgs& A, const Rows& R, const __half* sq, const float* sf, int t_end, int lane) {
     const int g = lane >> 2, q4 = lane & 3;
-    vref = rv = 0.0f;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -609,7 +625,7 @@ struct RowState {
         const int r = nb * 8 + 2 * q4 + i;
         f[nb][i] = sf[r];
         see[nb][i] = r < R.rows ? min(t_end, seen_by(A, R, r)) : t_end;
-        m[nb][i] = -INFINITY;
+        m[nb][i] = n[nb][i] = -INFINITY;
         l[nb][i] = 0.0f;
       }
 #pragma unroll
@@ -657,8 +673,9 @@ struct RowState {
       }
     }
     // factors to units of log2 (-inf stays -inf in a block of zeros); a new reference only where a lane's
-    // scores, or the value scale, grew by 2^kGrow: no exchange between lanes otherwise
-    float fac[2][NB][2], top[NB][2];
+    // scores, or weighted magnitudes, grew by 2^kGrow: no exchange between lanes otherwise
+    float fac[2][NB][2], top[NB][2], vtop[NB][2];
+    const float e0 = scale_exponent(md.sv[0]), e1 = scale_exponent(md.sv[1]);
     bool grow = false;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -666,31 +683,31 @@ struct RowState {
       for (int i = 0; i < 2; ++i) {
         fac[0][nb][i] = fmaxf(f[nb][i] * md.sk[0], FLT_MIN);
         fac[1][nb][i] = fmaxf(f[nb][i] * md.sk[1], FLT_MIN);
-        top[nb][i] = fmaxf(fmaxf(x[0][nb][i], x[0][nb][i + 2]) * fac[0][nb][i], fmaxf(x[1][nb][i], x[1][nb][i + 2]) * fac[1][nb][i]);
-        grow = grow || top[nb][i] > m[nb][i] + kGrow;
+        const float x0 = fmaxf(x[0][nb][i], x[0][nb][i + 2]) * fac[0][nb][i], x1 = fmaxf(x[1][nb][i], x[1][nb][i + 2]) * fac[1][nb][i];
+        top[nb][i] = fmaxf(x0, x1);
+        vtop[nb][i] = fmaxf(x0 + e0, x1 + e1);
+        grow = grow || top[nb][i] > m[nb][i] + kGrow || vtop[nb][i] > n[nb][i] + kGrow;
       }
-    const float vmax = fmaxf(md.sv[0], md.sv[1]);
-    if (__any_sync(0xffffffffu, grow || vmax > vref * kGrowFactor)) {
-      float fv = 1.0f;
-      if (vmax > vref * kGrowFactor) {
-        fv = __fdiv_rn(vref, vmax);
-        vref = vmax;
-        rv = __fdiv_rn(1.0f, vref);
-      }
+    if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         float b[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
-          for (int s = 4; s < 32; s <<= 1) top[nb][i] = fmaxf(top[nb][i], __shfl_xor_sync(0xffffffffu, top[nb][i], s));
-          b[i] = 1.0f;
+          for (int s = 4; s < 32; s <<= 1) {
+            top[nb][i] = fmaxf(top[nb][i], __shfl_xor_sync(0xffffffffu, top[nb][i], s));
+            vtop[nb][i] = fmaxf(vtop[nb][i], __shfl_xor_sync(0xffffffffu, vtop[nb][i], s));
+          }
           if (top[nb][i] > m[nb][i] + kGrow) {
-            b[i] = ex2(m[nb][i] - top[nb][i]);
-            l[nb][i] *= b[i];
+            l[nb][i] *= ex2(m[nb][i] - top[nb][i]);
             m[nb][i] = top[nb][i];
           }
-          b[i] *= fv;
+          b[i] = 1.0f;
+          if (vtop[nb][i] > n[nb][i] + kGrow) {
+            b[i] = ex2(n[nb][i] - vtop[nb][i]);
+            n[nb][i] = vtop[nb][i];
+          }
         }
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
@@ -702,16 +719,19 @@ struct RowState {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const float z0 = m[nb][0] == -INFINITY ? 0.0f : m[nb][0], z1 = m[nb][1] == -INFINITY ? 0.0f : m[nb][1];
+      // m - n <= 127: where m was set, n became at least m - 120 - kGrow
+      const float rel0 = ex2(fminf(z0 - n[nb][0], 127.0f)), rel1 = ex2(fminf(z1 - n[nb][1], 127.0f));
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        const float wv = md.sv[mt] * rv;
+        // finite, so that a weight of 0 stays 0 beside a scale that the row does not see
+        const float w0 = fminf(md.sv[mt] * rel0, FLT_MAX), w1 = fminf(md.sv[mt] * rel1, FLT_MAX);
         const float p0 = ex2(fmaf(x[mt][nb][0], fac[mt][nb][0], -z0)), p1 = ex2(fmaf(x[mt][nb][1], fac[mt][nb][1], -z1));
         const float p2 = ex2(fmaf(x[mt][nb][2], fac[mt][nb][0], -z0)), p3 = ex2(fmaf(x[mt][nb][3], fac[mt][nb][1], -z1));
         l[nb][0] += p0 + p2;
         l[nb][1] += p1 + p3;
         // [token][row] -> [row][token]: the column operand of the second product
-        pb[mt][nb][0] = transpose8x8(pack_half2(p0 * wv, p1 * wv));
-        pb[mt][nb][1] = transpose8x8(pack_half2(p2 * wv, p3 * wv));
+        pb[mt][nb][0] = transpose8x8(pack_half2(p0 * w0, p1 * w1));
+        pb[mt][nb][1] = transpose8x8(pack_half2(p2 * w0, p3 * w1));
       }
     }
 #pragma unroll
@@ -778,7 +798,6 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
   float* sf = reinterpret_cast<float*>(wml + kDecWarps * NR);              // [NR]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sf + NR);                   // [warp][NST]
   __shared__ int s_abort;
-  __shared__ float s_vref[kDecWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
   const int h = blockIdx.y, req = blockIdx.z, split = blockIdx.x;
   griddep_wait();
@@ -873,39 +892,40 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
     __syncwarp();
     if (k + NST < mine) issue(k + NST);
   }
-  // join the four warps: weights 2^(m_w - M) and the value reference of each
+  // join the four warps: each one's share of the CTA's rows
   S.publish(wml + warp * NR, lane);
-  if (lane == 0) s_vref[warp] = S.vref;
   __syncthreads();                                       // every ring is free: the accumulators go there
   constexpr int AP = D + 4;                              // row pitch of the accumulators
   float* acc = reinterpret_cast<float*>(ring);           // [warp][NR][AP]
   float* mine_o = acc + kDecWarps * NR * AP;             // [NR][D]: this CTA's joined rows
   float2* mine_ml = reinterpret_cast<float2*>(mine_o + NR * D);
   static_assert((kDecWarps * NR * AP + NR * D + 2 * NR) * 4 <= dec_ring_bytes(D), "the join fits the ring");
-  const auto weight = [&](int w, int r, float M) { const float x = wml[w * NR + r].x; return x == -INFINITY ? 0.0f : ex2(x - M); };
+  const auto total = [&](int r) {                        // maximum and sum of row r over the warps
+    float2 y = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) y.x = fmaxf(y.x, wml[w * NR + r].x);
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      const float2 u = wml[w * NR + r];
+      y.y += u.x == -INFINITY ? 0.0f : ex2(u.x - y.x) * u.y;
+    }
+    return y;
+  };
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = nb * 8 + 2 * q4 + i;
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, wml[w * NR + r].x);
-      const float wt = weight(warp, r, M) * s_vref[warp];
+      const float2 ml = total(r), u = result_factors(S.n[nb][i], ml.x, ml.y);
       float* p = acc + (warp * NR + r) * AP + (D / 8) * g;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
-        *reinterpret_cast<float2*>(p + 2 * j) = make_float2(S.o[j][nb][i] * wt, S.o[j][nb][i + 2] * wt);
+        *reinterpret_cast<float2*>(p + 2 * j) = make_float2(S.o[j][nb][i] * u.x * u.y, S.o[j][nb][i + 2] * u.x * u.y);
     }
   __syncthreads();
   for (int idx = tid; idx < NR * D / 4; idx += kDecWarps * 32) {
     const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
     if (r >= R.rows) break;
-    float M = -INFINITY, L = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, wml[w * NR + r].x);
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) L += weight(w, r, M) * wml[w * NR + r].y;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
@@ -913,7 +933,7 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
       v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
     }
     *reinterpret_cast<float4*>(mine_o + r * D + d) = v;
-    if (d == 0) mine_ml[r] = make_float2(M, L);
+    if (d == 0) mine_ml[r] = total(r);
   }
   // the cluster's CTAs in rank order, each taking its share of the values
   cluster_sync();
@@ -923,7 +943,6 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
     if (r >= R.rows) break;
     float2 ml[kMaxCluster];
     float M = -INFINITY, L = 0.0f;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int s = 0; s < kMaxCluster; ++s) {
       ml[s] = s < A.splits ? ld_cluster_f32x2(mapa_shared(ml_at + 8 * r, s)) : make_float2(-INFINITY, 0.0f);
@@ -931,15 +950,21 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
     }
 #pragma unroll
     for (int s = 0; s < kMaxCluster; ++s) {
+      ml[s].y *= ml[s].x == -INFINITY ? 0.0f : ex2(ml[s].x - M);
+      L += ml[s].y;
+    }
+    const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int s = 0; s < kMaxCluster; ++s) {
       if (s < A.splits) {
-        const float w = ml[s].x == -INFINITY ? 0.0f : ex2(ml[s].x - M);
+        const float w = ml[s].y * inv;
         const float4 y = ld_cluster_f32x4(mapa_shared(o_at + (r * D + d) * 4, s));
-        L += w * ml[s].y;
         v.x += w * y.x; v.y += w * y.y; v.z += w * y.z; v.w += w * y.w;
       }
     }
     const int token = R.a + r / A.G, head = h * A.G + r % A.G;
-    store_row4<DT>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + d, v, L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f);
+    store_row4<DT>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + d, v);
   }
   cluster_sync();                                        // nobody leaves while its rows are read
 }
@@ -1107,7 +1132,6 @@ struct FlatSmem {
   int2 ids[kDecWarps][2 * kDecGroup];
   float2 ml[kDecWarps][8 * NB];
   float f[8 * NB];
-  float vref[kDecWarps];
   uint64_t bars[kDecWarps][kDecStages];
   int abort;
 };
@@ -1222,12 +1246,16 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_flat_kernel(const AttnAr
       __syncwarp();
       send();
     }
-    // join the four warps in order: weights 2^(m_w - M) and the value reference of each
+    // join the four warps in order: each one's share of the rows
     S.publish(X.ml[warp], lane);
-    if (lane == 0) X.vref[warp] = S.vref;
     __syncthreads();
-    const auto top = [&](int r) { return fmaxf(fmaxf(X.ml[0][r].x, X.ml[1][r].x), fmaxf(X.ml[2][r].x, X.ml[3][r].x)); };
-    const auto weight = [&](int w, int r, float M) { const float x = X.ml[w][r].x; return x == -INFINITY ? 0.0f : ex2(x - M); };
+    const auto total = [&](int r) {                        // maximum and sum of row r over the warps
+      const float M = fmaxf(fmaxf(X.ml[0][r].x, X.ml[1][r].x), fmaxf(X.ml[2][r].x, X.ml[3][r].x));
+      float L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) L += X.ml[w][r].x == -INFINITY ? 0.0f : ex2(X.ml[w][r].x - M) * X.ml[w][r].y;
+      return make_float2(M, L);
+    };
     static_assert(kDecWarps == 4, "the join is written for four warps");
 #pragma unroll 1
     for (int w = 0; w < kDecWarps; ++w) {
@@ -1237,13 +1265,13 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_flat_kernel(const AttnAr
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int r = nb * 8 + 2 * (lane & 3) + i;
-            const float wt = weight(w, r, top(r)) * X.vref[w];
+            const float2 ml = total(r), u = result_factors(S.n[nb][i], ml.x, ml.y);
             // rows 16 bytes and lanes 8 bytes apart: no two lanes of a half warp on one bank
             float2* p = reinterpret_cast<float2*>(&X.sum[r][2 * (lane >> 2)]);
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
               const float2 v = w == 0 ? make_float2(0.0f, 0.0f) : p[8 * j];
-              p[8 * j] = make_float2(v.x + S.o[j][nb][i] * wt, v.y + S.o[j][nb][i + 2] * wt);
+              p[8 * j] = make_float2(v.x + S.o[j][nb][i] * u.x * u.y, v.y + S.o[j][nb][i + 2] * u.x * u.y);
             }
           }
       }
@@ -1254,20 +1282,16 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_flat_kernel(const AttnAr
     for (int idx = tid; idx < NR * D / 4; idx += kDecWarps * 32) {
       const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
       if (r >= R.rows) break;
-      const float M = top(r);
-      float L = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) L += weight(w, r, M) * X.ml[w][r].y;
       const int at = 2 * (4 * (d % (D / 8)) + d / (D / 8));
       const float2 v0 = *reinterpret_cast<const float2*>(&X.sum[r][at]), v1 = *reinterpret_cast<const float2*>(&X.sum[r][at + 16]);
       const float4 v = make_float4(v0.x, v0.y, v1.x, v1.y);
       if (I.out == kItemWhole) {
         const int token = R.a + r / A.G, head = I.h * A.G + r % A.G;
-        store_row4<DT>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + d, v, L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f);
+        store_row4<DT>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + d, v);
       } else {
         const size_t cell = ((size_t)blockIdx.x * 2 + I.out) * NR + r;
         *reinterpret_cast<float4*>(A.part_o + cell * D + d) = v;
-        if (d == 0) *reinterpret_cast<float2*>(A.part_ml + cell * 2) = make_float2(M, L);
+        if (d == 0) *reinterpret_cast<float2*>(A.part_ml + cell * 2) = total(r);
       }
     }
   }
@@ -1280,15 +1304,14 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_flat_kernel(const AttnAr
 // columns, O += P V (P from TMEM; V as it lies, token rows of 64 d, an MN-major
 // operand).  Roles:
 //   warps 0-3, 4-7   softmax of row tile 0 / 1, a row per thread: maximum, weights,
-//                    sum; rescales O only when a maximum (or the largest value scale)
-//                    grew by more than 2^7 (weights stay below 2^14 in fp16); output
+//                    sum; rescales O only when the largest weighted magnitude grew
+//                    by more than 2^7; output
 //   warps 8-11       codes -> fp16 (the next tile's codes already in registers)
 //                    of an item and, ahead of it, the queries of the next one
 //   warp 12          issues the MMAs: S0 S1 | P0V S0' | P1V S1' | ...
 //   warp 13          walks the schedule, up to eight items ahead
-// The value scale goes into a weight's exponent, p' = 2^(x - m + log2 s_v - v) with v
-// the log2 of the largest value scale so far (up to 2^7), so it costs nothing per
-// weight; the row sum takes each 16 tokens' sum times 2^v / s_v.  2048 rows x 32 heads
+// The value scale goes into a weight's exponent, p' = 2^(x + log2 s_v - n), so it costs
+// nothing per weight; the row sum takes each 16 tokens' sum times 2^(n - m) / s_v.  2048 rows x 32 heads
 // at 16384 tokens, d = 128: 610 us, 845 TFLOP/s.  Bound by the softmax warps, two a
 // scheduler: 3300 cycles a tile each where the exponentials alone take 1100.  144, 128
 // and 96 registers: a spilled value misses what is left of L1 and costs 600 cycles.
@@ -1490,7 +1513,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
         if (rl < rows) see = seen_by(A, R, I.r0 + rt * 128 + rl);
         clear = seen_by(A, R, I.r0 + rt * 128);
       }
-      float m = -INFINITY, l = 0.0f, lv = -INFINITY;
+      float m = -INFINITY, l = 0.0f, n = -INFINITY;
       const float f = sf[rt * 128 + rl];
       bool ok = true;
       for (int j = lo; j < end; ++j, ++n_s) {
@@ -1528,17 +1551,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
             t0 = fmaxf(fmaxf(t0, at(i + 12)), at(i + 13));
             t1 = fmaxf(fmaxf(t1, at(i + 14)), at(i + 15));
             // -inf stays -inf in a block of zeros
-            top = fmaxf(top, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * fmaxf(f * sk_of(g), FLT_MIN));
-            vtop = fmaxf(vtop, lsv_of(g));
+            const float x = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * fmaxf(f * sk_of(g), FLT_MIN);
+            top = fmaxf(top, x);
+            vtop = fmaxf(vtop, x + lsv_of(g));             // of what the row sees: -inf elsewhere
           }
           // new references only where one grew by 2^kGrow (or is the first)
-          const bool grow = top > m + kGrow, vgrow = vtop > lv + kGrow;   // -inf: any finite one
+          const bool grow = top > m + kGrow, vgrow = vtop > n + kGrow;   // -inf: any finite one
           if (__any_sync(0xffffffffu, grow || vgrow)) {
-            const float m1 = grow ? ceilf(top) : m, lv1 = vgrow ? ceilf(vtop) : lv;
-            const float b = m1 == m ? 1.0f : power_of_two(m - m1), bo = lv1 == lv ? b : b * power_of_two(lv - lv1);
-            l *= b;
+            const float m1 = grow ? ceilf(top) : m, n1 = vgrow ? ceilf(vtop) : n;
+            const float bo = n1 == n ? 1.0f : power_of_two(n - n1);
+            l *= m1 == m ? 1.0f : power_of_two(m - m1);
             m = m1;
-            lv = lv1;
+            n = n1;
             if (j > lo || q == 1) {
               // the first half's products of this tile may be under way
               if (q == 1 && !(ok = mbar_wait(&o1_full[rt], n_s & 1, &s_abort))) break;
@@ -1554,15 +1578,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
               }
             }
           }
-          const float z = m == -INFINITY ? 0.0f : m, vz = lv == -INFINITY ? 0.0f : lv;
+          // an exponent below that of 2^-60 p counts as that: its values are lost beside the largest weighted one
+          // either way, and the sum still gets p back
+          const float z = m == -INFINITY ? 0.0f : m, nz = n == -INFINITY ? 0.0f : n, least = -60.0f - z;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            // a scale below 2^-60 of the largest counts as that: its values are lost beside it either way
-            const float ls0 = fmaxf(lsv_of(2 * h), vz - 60.0f) - vz, ls1 = fmaxf(lsv_of(2 * h + 1), vz - 60.0f) - vz;
+            const float e0 = fmaxf(lsv_of(2 * h) - nz, least), e1 = fmaxf(lsv_of(2 * h + 1) - nz, least);
             const float a0 = fmaxf(f * sk_of(2 * h), FLT_MIN), a1 = fmaxf(f * sk_of(2 * h + 1), FLT_MIN);
-            const float r0 = ex2(-ls0), r1 = ex2(-ls1);
+            const float r0 = ex2(-z - e0), r1 = ex2(-z - e1);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) y[h][i] = __float_as_uint(ex2(fmaf(__uint_as_float(y[h][i]), i < 16 ? a0 : a1, (i < 16 ? ls0 : ls1) - z)));
+            for (int i = 0; i < 32; ++i) y[h][i] = __float_as_uint(ex2(fmaf(__uint_as_float(y[h][i]), i < 16 ? a0 : a1, i < 16 ? e0 : e1)));
             uint32_t p[16];
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -1594,7 +1619,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
         ++n_o;
         tc_fence_after();
       }
-      const float u = lv == -INFINITY ? 0.0f : ex2(lv) * kUnit<FMT>, mul = whole ? (l > 0.0f ? __fdiv_rn(u, l) : 0.0f) : u;
+      const float2 u = result_factors(n, m, l);
       const size_t cell = ((size_t)blockIdx.x * 2 + (whole ? 0 : I.out)) * kTileRows + rt * 128 + rl;
       const int r = I.r0 + rt * 128 + rl, token = I.a + r / A.G, head = I.h * A.G + r % A.G;
       if (!whole) *reinterpret_cast<float2*>(A.part_ml + cell * 2) = make_float2(m, l);
@@ -1611,7 +1636,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
         if (live) {
           float y[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]) * mul;
+          for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]) * (u.x * kUnit<FMT>) * u.y;
           if (whole) {
             uint4* dst = reinterpret_cast<uint4*>(A.out + (int64_t)token * A.out_stride + (int64_t)head * D + 32 * q);
 #pragma unroll
@@ -1858,7 +1883,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
   }
 }
 
-// Adds the pieces of the items that a border of the schedule cut: blockIdx.x is the
+// Joins the pieces of the items that a border of the schedule cut: blockIdx.x is the
 // CTA whose last item continues in the CTAs after it, blockIdx.y a part of its rows,
 // `wide` warps a row (warp w of them takes every wide-th piece; then the warps in
 // order).  One warp a row where an item has a few pieces, all eight where a long
@@ -1914,15 +1939,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnA
       }
 #pragma unroll
       for (int b = 0; b < kAhead; ++b) top = fmaxf(top, ml[b].x);
-      const float back = m == -INFINITY ? 0.0f : ex2(m - top);
+      const float old = m == -INFINITY ? 0.0f : ex2(m - top) * l;
       m = top;
-      l *= back;
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] *= back;
+      l = old;
 #pragma unroll
       for (int b = 0; b < kAhead; ++b) {
-        const float w = ml[b].x == -INFINITY ? 0.0f : ex2(ml[b].x - m);
-        l += w * ml[b].y;
+        ml[b].y *= ml[b].x == -INFINITY ? 0.0f : ex2(ml[b].x - m);
+        l += ml[b].y;
+      }
+      const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= old * inv;
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) {
+        const float w = ml[b].y * inv;
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] += w * x[b][i];
       }
@@ -1936,25 +1966,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnA
       if (sub > 0) continue;
       float M = m;
       for (int w = 1; w < wide; ++w) M = fmaxf(M, s_ml[warp + w].x);
-      const float own = m == -INFINITY ? 0.0f : ex2(m - M);
-      l *= own;
+      const auto part = [&](const float2& ml) { return ml.x == -INFINITY ? 0.0f : ex2(ml.x - M) * ml.y; };
+      const float own = part(make_float2(m, l));
+      float all = own;
+      for (int w = 1; w < wide; ++w) all += part(s_ml[warp + w]);
+      const float inv = all > 0.0f ? __fdiv_rn(1.0f, all) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] *= own;
+      for (int i = 0; i < V; ++i) v[i] *= own * inv;
       for (int w = 1; w < wide; ++w) {
-        const float2 ml = s_ml[warp + w];
-        const float b = ml.x == -INFINITY ? 0.0f : ex2(ml.x - M);
-        l += b * ml.y;
+        const float b = part(s_ml[warp + w]) * inv;
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] += b * s_v[warp + w][V * lane + i];
       }
     }
     if (!mine) continue;
     const int row = P.r0 + r;
-    const float mul = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
     uint16_t* dst = A.out + (int64_t)(P.token + row / A.G) * A.out_stride + (int64_t)(P.h * A.G + row % A.G) * D + V * lane;
     uint32_t w[V / 2];
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) w[i] = (uint32_t)store16<DT>(v[2 * i] * mul) | ((uint32_t)store16<DT>(v[2 * i + 1] * mul) << 16);
+    for (int i = 0; i < V / 2; ++i) w[i] = (uint32_t)store16<DT>(v[2 * i]) | ((uint32_t)store16<DT>(v[2 * i + 1]) << 16);
     if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(dst) = w[0];
   }

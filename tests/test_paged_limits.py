@@ -106,6 +106,60 @@ def test_plan_refuses_more_blocks_than_the_ring_has_room_for(gpu):
     assert np.array_equal(out.cpu().numpy(), want["state"])
 
 
+# ------------------------------------------------- value scales far apart
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
+@pytest.mark.parametrize("fmt,dtype", BOTH_FORMATS)
+def test_rows_do_not_depend_on_what_they_do_not_see(gpu, heads, kv, d, bs, new, lens, fmt, dtype):
+    """Other keys and values, with scales 2^4 to 2^30 larger, in the blocks that only later rows see: the same bits."""
+    import torch
+    P, table = pool(sum(lens), heads, kv, d, bs, lens, fmt, dtype)
+    q = normal(P.rng, sum(new), heads * d, dtype)
+    base, got, want, tol = both(P, q, new, lens, table, dtype=dtype)
+    within(got, want, tol)
+    starts, blind = np.concatenate([[0], np.cumsum(new)]), []
+    for i, (m, L) in enumerate(zip(new, lens)):
+        lead = (L - 1) // bs * bs                          # the last block's first token
+        blind += [starts[i] + j for j in range(m) if L - m + j + 1 <= lead]
+    assert len(blind) >= len(new)
+    P2, _ = pool(77, heads, kv, d, bs, lens, fmt, dtype)
+    for power in (4, 30):
+        if dtype == "fp16" and power > 4:
+            continue                                       # the later rows' results would not be fp16 numbers
+        for i, L in enumerate(lens):
+            blk = int(table[i, (L - 1) // bs])
+            P.codes[:, blk] = P2.codes[:, blk]
+            P.scale[:, blk] = P2.scale[:, blk] * np.array([[1.0], [2.0 ** power]], np.float32)
+        bits, got, want, tol = both(P, q, new, lens, table, dtype=dtype)
+        assert torch.equal(bits[blind], base[blind])
+        within(got, want, tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
+@pytest.mark.parametrize("fmt,dtype", BOTH_FORMATS)
+@pytest.mark.parametrize("causal", [True, False])
+def test_large_values_of_no_weight(gpu, heads, kv, d, bs, new, lens, fmt, dtype, causal):
+    """Every third block holds values 2^40 larger at scores 60 below the others': weights of e^-60 leave nothing of them,
+    and what the others add keeps its bits.  Every fifth holds values 2^30 smaller."""
+    P, table = pool(sum(lens) + 1, heads, kv, d, bs, lens, fmt, dtype)
+    n = sum(new)
+    q = normal(P.rng, n, heads * d, dtype).abs() * 0.25 + 0.75
+    q = q.to(dtype_of(dtype)).float()
+    low = np.zeros(P.n, bool)
+    for i in range(len(lens)):
+        low[table[i, 1::3]] = True
+        P.scale[1, table[i, 2::5]] *= np.float32(2.0 ** -30)
+    low[table[:, 0]] = False                               # every row sees a block of ordinary scores
+    P.codes[0, low] = pk.to_codes(np.full((1,), -127.0), fmt)[0]
+    P.scale[0, low] = 60.0 / (d ** 0.5 * 127.0 * 0.75)     # q >= 0.75: scores of -60 or less
+    P.scale[1, low] *= np.float32(2.0 ** 40)
+    P.scale[0, ~low] *= np.float32(0.25)
+    _, got, want, tol = both(P, q, new, lens, table, causal, dtype)
+    within(got, want, tol)
+    assert np.abs(got).max() < 1000
+
+
 # ---------------------------------------------------- the smallest and the largest numbers
 @pytest.mark.gpu
 @pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
@@ -117,3 +171,37 @@ def test_queries_of_extreme_size(gpu, heads, kv, d, bs, new, lens, fmt, power):
     P.scale[0] = (P.scale[0].astype(np.float64) * 2.0 ** (-power if power > 0 else min(-power, 112))).astype(np.float32)
     _, got, want, tol = both(P, normal(P.rng, sum(new), heads * d, power=power), new, lens, table)
     within(got, want, tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("where", ["first", "all", "last"])
+def test_values_of_subnormal_size(gpu, heads, kv, d, bs, new, lens, fmt, where):
+    """Blocks as an append leaves them for values of 1 to 3 times 2^-133 (scales near 2^-140), before, without and behind
+    ordinary ones."""
+    P, table = pool(sum(lens) + 2, heads, kv, d, bs, lens, fmt, "bf16")
+    for i, L in enumerate(lens):
+        nb = -(-L // bs)
+        for c in {"first": range(0, max(1, nb // 2)), "all": range(nb), "last": range(nb // 2, nb)}[where]:
+            blk = int(table[i, c])
+            x = (P.rng.integers(1, 4, size=(bs, kv, d)) * np.where(P.rng.random((bs, kv, d)) < 0.5, 1, -1)) * 2.0 ** -133
+            P.codes[1], P.scale[1] = pk.append(x, np.arange(blk * bs, (blk + 1) * bs), [0, bs], P.codes[1], P.scale[1], fmt)
+            assert 0 < P.scale[1, blk].max() < 2.0 ** -137
+    _, got, want, tol = both(P, normal(P.rng, sum(new), heads * d), new, lens, table)
+    within(got, want, tol)
+    if where == "all":
+        assert np.abs(got).max() <= 2.0 ** -131
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
+def test_values_near_the_largest(gpu, heads, kv, d, bs, new, lens):
+    """Values up to 2^126 and uniform weights: a mean of finite values is finite."""
+    P, table = pool(sum(lens) + 4, heads, kv, d, bs, lens, "int8", "bf16")
+    P.codes[1] = np.abs(P.codes[1].view(np.int8)).view(np.uint8)
+    P.scale[1] = np.float32(2.0 ** 119)
+    P.scale[0] *= np.float32(2.0 ** -20)
+    _, got, want, tol = both(P, normal(P.rng, sum(new), heads * d), new, lens, table)
+    within(got, want, tol)
+    assert np.abs(got).max() > 2.0 ** 120
