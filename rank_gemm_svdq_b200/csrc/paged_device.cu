@@ -1136,8 +1136,16 @@ struct FlatSmem {
   int abort;
 };
 
+// CTAs an SM, which the schedule is sized by: four with 64 values a head and 8 rows; the accumulators of 16 rows, or
+// the ring of 128 values, leave three, both two.  The launch bounds hold the compiler to it, the assertion the ring.
+// 64 requests of up to 4096 tokens, 4 heads of 64 values, 16 query heads each: 47 us; with a grid for four CTAs an SM,
+// of which three fit, 53 us, and one request of 131071 tokens 48 instead of 35 us (graphs, warm L2).
+constexpr int flat_per_sm(int head_dim, int rows) { return 4 - (head_dim > 64) - (rows > 8); }
+constexpr int kSmemPerSm = 228 * 1024, kSmemPerCta = 1024;   // what an SM has, and what it takes for itself for each CTA
+
 template <int DT, int FMT, int D, int NB>
-__global__ void __launch_bounds__(kDecWarps * 32) paged_flat_kernel(const AttnArgs A) {
+__global__ void __launch_bounds__(kDecWarps * 32, flat_per_sm(D, 8 * NB)) paged_flat_kernel(const AttnArgs A) {
+  static_assert(flat_per_sm(D, 8 * NB) * (sizeof(FlatSmem<D, NB>) + kSmemPerCta + 256) <= kSmemPerSm, "the rings fit");
   constexpr int NST = kDecStages, kStage = dec_stage_bytes(D), NR = 8 * NB;
   extern __shared__ __align__(128) uint8_t dsm[];
   FlatSmem<D, NB>& X = *reinterpret_cast<FlatSmem<D, NB>*>(dsm);
@@ -2091,7 +2099,6 @@ constexpr int kSplitSms = 148;
 // over as many CTAs as are resident at once.  More rows: the tensor-core kernel (rows
 // 256), a CTA per SM.  No CTA of a schedule is left with less than a token tile.
 struct Split { int rows, ctas, cluster, snap; };
-constexpr int flat_per_sm(int head_dim, int rows) { return head_dim == 64 ? 4 : rows == 8 ? 3 : 2; }
 Split split_of(const svdq_paged_cache* c, const svdq_paged_batch* b) {
   const int64_t G = c->heads / c->kv_heads, rows = b->max_new * G, cells = (int64_t)b->B * c->kv_heads;
   const int64_t len = std::max(b->max_len, 1), tiles = (len + kTileTok - 1) / kTileTok;

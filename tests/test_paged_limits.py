@@ -205,3 +205,14 @@ def test_values_near_the_largest(gpu, heads, kv, d, bs, new, lens):
     _, got, want, tol = both(P, normal(P.rng, sum(new), heads * d), new, lens, table)
     within(got, want, tol)
     assert np.abs(got).max() > 2.0 ** 120
+
+
+# ------------------------------------------------------------- the schedule's size
+def test_the_schedule_has_as_many_parts_as_are_resident():
+    """9 to 16 rows of 64 values: three CTAs of the balanced schedule fit an SM (168 registers a thread of 128), not four."""
+    import ctypes
+    for d, G, per_sm in ((64, 8, 4), (64, 16, 3), (128, 8, 3), (128, 16, 2)):
+        c = sv.svdq_paged_cache(4096, 4096, 4096, 4096, 4 * G, 4, d, 64, 1 << 16, 1, sv.BF16, 0)
+        b = sv.svdq_paged_batch(4096, 4096, 4096, None, 100, 600, 100, 1, 30000, 0)
+        got = sv.lib().svdq_paged_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(b))
+        assert got == 148 * per_sm * 2 * (32 + G * (d + 2) * 4), (d, G)
