@@ -445,6 +445,12 @@ __device__ __forceinline__ Rows request_rows(const AttnArgs& A, int i, bool note
   R.rows = R.n * A.G;
   return R;
 }
+// A block number of a request's table: -1, and recorded, where it lies outside the pool.
+__device__ __forceinline__ int pool_block(const AttnArgs& A, int id) {
+  if (id >= 0 && id < A.n_blocks) return id;
+  record_status(SVDQ_ERR_INVALID_ARG);
+  return -1;
+}
 // Tokens that row r sees (its new token is r / G).
 __device__ __forceinline__ int seen_by(const AttnArgs& A, const Rows& R, int r) {
   return A.causal ? max(0, R.L - R.n + r / A.G + 1) : R.L;
@@ -831,10 +837,8 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
       if (k < mine) {
         const int t = t_begin + (warp + kDecWarps * k) * kDecTile, c0 = t >> A.lb, c1 = (t + 16) >> A.lb;
         const int* row = A.table + (size_t)req * A.max_blocks;
-        id.x = row[c0];
-        id.y = c1 == c0 ? id.x : (c1 < nblk ? row[c1] : -2);
-        if (id.x < 0 || id.x >= A.n_blocks) { id.x = -1; record_status(SVDQ_ERR_INVALID_ARG); }
-        if (id.y != -2 && (id.y < 0 || id.y >= A.n_blocks)) { id.y = -1; record_status(SVDQ_ERR_INVALID_ARG); }
+        id.x = pool_block(A, row[c0]);
+        id.y = c1 == c0 ? id.x : (c1 < nblk ? pool_block(A, row[c1]) : -1);
         if (id.x >= 0) { const size_t c = (size_t)id.x * A.kv + h; m.sk[0] = A.ks[c]; m.sv[0] = A.vs[c]; }
         if (id.y >= 0) { const size_t c = (size_t)id.y * A.kv + h; m.sk[1] = A.ks[c]; m.sv[1] = A.vs[c]; }
       }
@@ -1194,10 +1198,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, flat_per_sm(D, 8 * NB)) paged_
         DecMeta m = {{0.0f, 0.0f}, {0.0f, 0.0f}};
         if (tt < t_end) {
           const int nblk = blocks_of(t_end, A.lb), c0 = tt >> A.lb, c1 = (tt + 16) >> A.lb;
-          id.x = row[c0];
-          id.y = c1 == c0 ? id.x : (c1 < nblk ? row[c1] : -2);
-          if (id.x < 0 || id.x >= A.n_blocks) { id.x = -1; record_status(SVDQ_ERR_INVALID_ARG); }
-          if (id.y != -2 && (id.y < 0 || id.y >= A.n_blocks)) { id.y = -1; record_status(SVDQ_ERR_INVALID_ARG); }
+          id.x = pool_block(A, row[c0]);
+          id.y = c1 == c0 ? id.x : (c1 < nblk ? pool_block(A, row[c1]) : -1);
           if (id.x >= 0) { const size_t c = (size_t)id.x * A.kv + h; m.sk[0] = A.ks[c]; m.sv[0] = A.vs[c]; }
           if (id.y >= 0) { const size_t c = (size_t)id.y * A.kv + h; m.sk[1] = A.ks[c]; m.sv[1] = A.vs[c]; }
         }
@@ -1695,16 +1697,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int b = (t + 16 * i) >> A.lb;
-        N.id[i] = b < nblk ? row[b] : -2;                  // -2: past the request's blocks
+        N.id[i] = b < nblk ? row[b] : -1;                  // past the request's blocks
       }
       return true;
     };
-    // codes and scales of tile N (scales: lanes 0-15 and 16-31 hold the first group's and the second's)
+    // codes and scales of tile N, the one that advance came to last (scales: lanes 0-15 and 16-31 hold the first
+    // group's and the second's)
     const auto load = [&](Next N) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (N.id[i] == -1 || N.id[i] < -2 || N.id[i] >= A.n_blocks) {
-          record_status(SVDQ_ERR_INVALID_ARG);
+        if (N.id[i] < 0 || N.id[i] >= A.n_blocks) {
+          if ((j * kTileTok + 32 * w + 16 * i) >> A.lb < nblk) record_status(SVDQ_ERR_INVALID_ARG);
           N.id[i] = -1;
         }
       }

@@ -207,6 +207,25 @@ def test_values_near_the_largest(gpu, heads, kv, d, bs, new, lens):
     assert np.abs(got).max() > 2.0 ** 120
 
 
+# --------------------------------------------------------------- bad pages
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
+@pytest.mark.parametrize("number", [-1, -2, -3, -2 ** 31, 2 ** 31 - 1])
+def test_every_bad_block_number_is_recorded(gpu, heads, kv, d, bs, new, lens, number):
+    """One bad number, in an even or an odd place of the table: left out and recorded."""
+    for place in (0, 1):
+        P, table = pool(sum(lens) + 5, heads, kv, d, bs, lens, "int8", "bf16")
+        table[-1, place] = number
+        _, got, want, tol = both(P, normal(P.rng, sum(new), heads * d), new, lens, table)
+        within(got, want, tol)
+        assert sv.get_status() == sv.ERR_INVALID_ARG and sv.get_status() == sv.OK
+    P, table = pool(sum(lens) + 5, heads, kv, d, bs, lens, "int8", "bf16")
+    for i, L in enumerate(lens):
+        table[i, -(-L // bs):] = number                    # past the request's blocks: not read
+    both(P, normal(P.rng, sum(new), heads * d), new, lens, table)
+    assert sv.get_status() == sv.OK
+
+
 # ------------------------------------------------------------- the schedule's size
 def test_the_schedule_has_as_many_parts_as_are_resident():
     """9 to 16 rows of 64 values: three CTAs of the balanced schedule fit an SM (168 registers a thread of 128), not four."""
