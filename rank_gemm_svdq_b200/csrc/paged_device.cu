@@ -232,12 +232,14 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
   }
 }
 
-// x / s as IEEE division rounds it: q = RN(x rs) is within an ulp, e = x - q s is
-// exact (one FMA), RN(q + e rs) is the correctly rounded quotient (Markstein) while
-// nothing under- or overflows: for 2^-60 <= s <= 2^60, rs = RN(1 / s).
+// x / s as IEEE division rounds it: q = RN(x rs) is within an ulp, e = q s - x is
+// exact (one FMA), RN(q - e rs) is the correctly rounded quotient (Markstein) while
+// nothing under- or overflows: for 2^-60 <= s <= 2^60, rs = RN(1 / s).  e is +0 where
+// the quotient is exact, and -e rs + q then keeps the sign of a zero q (with x - q s
+// for e a quotient of -0 came out as +0, another E4M3 code).
 __device__ __forceinline__ float quotient(float x, float s, float rs) {
   const float q = __fmul_rn(x, rs);
-  return __fmaf_rn(__fmaf_rn(-q, s, x), rs, q);
+  return __fmaf_rn(-__fmaf_rn(q, s, -x), rs, q);
 }
 
 __device__ __noinline__ float divide_rn(float x, float s) { return __fdiv_rn(x, s); }

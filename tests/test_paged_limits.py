@@ -207,6 +207,27 @@ def test_values_near_the_largest(gpu, heads, kv, d, bs, new, lens):
     assert np.abs(got).max() > 2.0 ** 120
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -70, 2.0 ** 70])
+def test_append_keeps_the_sign_of_zero(gpu, fmt, size):
+    """-0 is the code of -0 (E4M3: 0x80), whatever the block's scale."""
+    import torch
+    bs, d = 16, 64
+    x = np.linspace(-1, 1, 2 * bs * d).reshape(2 * bs, 1, d) * size
+    x[:, :, ::3], x[:, :, 1::3] = -0.0, 0.0
+    x = torch.from_numpy(x).to(torch.bfloat16)
+    P = Pool(1, 1, 1, d, bs, 3, fmt, "bf16")
+    slots = np.arange(2 * bs, dtype=np.int32)
+    want = pk.append(x.double().numpy(), slots, [0, 2 * bs], P.codes[0], P.scale[0], fmt)
+    assert fmt == "int8" or (want[0][:2, :, :, ::3] == 0x80).all()
+    c = P.to_device()
+    b = sv.paged_batch(dev(np.array([[0, 1]], np.int32)), dev(np.array([32], np.int32)), dev(np.array([0, 32], np.int32)), dev(slots),
+                       max_new=32, max_len=32)
+    sv.paged_append(c, b, x.cuda(), x.cuda())
+    assert np.array_equal(P.t[0].cpu().numpy(), want[0]) and np.array_equal(P.t[1].cpu().numpy(), want[1])
+
+
 # --------------------------------------------------------------- bad pages
 @pytest.mark.gpu
 @pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
