@@ -307,11 +307,13 @@ svdq_status svdq_paged_plan(const svdq_paged_batch* b, int32_t block_size, int32
  *                                     whose first row is new)
  *   code = round(x / s);  earlier rows, when s grew: code = round(code (s_old / s)).
  * A block of zeros has s = 0.  Inputs finite.
- * Slots: those of one request follow one another within a block, as the plan
- * writes them, and a block takes the new tokens of one request; a token whose
- * slot is -1, or not next to the previous one in its block, is left out.  A slot
- * past the pool is skipped, and more than max_new new tokens of a request may be
- * left out; both are recorded for svdq_get_status (SVDQ_ERR_INVALID_ARG).
+ * Slots: a token whose slot is -1 is left out, wherever in the request it stands (a
+ * prefix that is cached already).  The others lie as the plan puts them: token k of a request
+ * in row (row of its token 0 + k) mod block_size, block after block, and a block
+ * takes the new tokens of one request; the rows before the first one written count as
+ * held before.  A token whose slot lies elsewhere, or past the pool, is
+ * left out, and more than max_new new tokens of a request may be; each is recorded for
+ * svdq_get_status (SVDQ_ERR_INVALID_ARG).
  * One kernel.  Errors: SVDQ_ERR_INVALID_ARG, SVDQ_ERR_ALIGNMENT,
  * SVDQ_ERR_UNSUPPORTED, SVDQ_ERR_CUDA.
  */

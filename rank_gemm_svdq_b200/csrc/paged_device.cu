@@ -279,6 +279,24 @@ struct AppendArgs {
   int B, n_tokens, kv, n_blocks, max_new, per;   // per: spare work indices a request
 };
 
+// The first token of [from, to) that has a slot, or `to`.  Called by all threads of the CTA, where a token without a
+// slot stands at a place that others follow from; apart, so that the usual call's registers do not pay for it.
+template <int THREADS>
+__device__ __noinline__ int first_with_slot(const int* slots, int from, int to) {
+  __shared__ int s_first;
+  for (; from < to; from += THREADS) {
+    const int t = from + threadIdx.x;
+    if (threadIdx.x == 0) s_first = INT_MAX;
+    __syncthreads();
+    if (t < to && slots[t] >= 0) atomicMin(&s_first, t);
+    __syncthreads();
+    const int first = s_first;
+    __syncthreads();
+    if (first != INT_MAX) return first;
+  }
+  return to;
+}
+
 template <int DT, int FMT, int D, int LB>
 __global__ void __launch_bounds__(append_threads(1 << LB, D), 768 / append_threads(1 << LB, D)) paged_append_kernel(const AppendArgs A) {
   constexpr int kAppendThreads = append_threads(1 << LB, D);
@@ -298,18 +316,31 @@ __global__ void __launch_bounds__(append_threads(1 << LB, D), 768 / append_threa
   const int a = clampi(A.cu[i], 0, A.n_tokens), e = clampi(A.cu[i + 1], 0, A.n_tokens);
   if (a >= e) return;
   if (e - a > A.max_new && tid == 0) record_status(SVDQ_ERR_INVALID_ARG);
-  const int j = w - (a >> LB) - A.per * i, o0 = A.slots[a] & (BS - 1);
+  // o0: row of the request's first token in its block, from the first one that has a slot
+  int lead = a, slot0 = A.slots[a];
+  if (slot0 < 0) {
+    lead = first_with_slot<kAppendThreads>(A.slots, a, e);
+    if (lead == e) return;
+    slot0 = A.slots[lead];
+  }
+  const int j = w - (a >> LB) - A.per * i, o0 = (slot0 - (lead - a)) & (BS - 1);
   const int64_t first = (int64_t)a + (j == 0 ? 0 : (int64_t)j * BS - o0);
   if (first >= e) return;
-  const int t0 = (int)first;
-  const int slot0 = A.slots[t0];
-  if (slot0 < 0) return;                             // a padded token
+  // this item's tokens [t0, end), from the first one that has a slot
+  int t0 = (int)first;
+  const int end = min(e, a + (j + 1) * BS - o0);
+  slot0 = A.slots[t0];
+  if (slot0 < 0) {
+    t0 = first_with_slot<kAppendThreads>(A.slots, t0, end);
+    if (t0 == end) return;
+    slot0 = A.slots[t0];
+  }
   const int blk = slot0 >> LB, off = slot0 & (BS - 1);
   if (blk >= A.n_blocks) {
     if (tid == 0) record_status(SVDQ_ERR_INVALID_ARG);
     return;
   }
-  const int rows = min(min(e, a + (j + 1) * BS - o0) - t0, BS - off);
+  const int rows = min(end - t0, BS - off);
   const int c = tid % kPerRow, r0 = tid / kPerRow;
   // chosen, not indexed: an index into the arguments would copy them to local memory
   const int64_t stride = which ? A.stride[1] : A.stride[0];
@@ -320,8 +351,8 @@ __global__ void __launch_bounds__(append_threads(1 << LB, D), 768 / append_threa
   uint4 v[kPass];
   int at[kPass];
   uint32_t have = 0;
-  // rows and their slots at once; a row counts only where the slot map puts it next to
-  // the block's first new row
+  // rows and their slots at once; a row counts only where the slot map puts it as far
+  // from the block's first new row as its token is from that one's
 #pragma unroll
   for (int p = 0; p < kPass; ++p) {
     const int r = r0 + p * kRows;
@@ -332,11 +363,17 @@ __global__ void __launch_bounds__(append_threads(1 << LB, D), 768 / append_threa
       at[p] = A.slots[t0 + r];
     }
   }
+  bool astray = ((slot0 - o0 - (t0 - a)) & (BS - 1)) != 0;
 #pragma unroll
   for (int p = 0; p < kPass; ++p) {
-    if (at[p] == slot0 + r0 + p * kRows) have |= 1u << p;
-    else v[p] = make_uint4(0, 0, 0, 0);
+    if (at[p] == slot0 + r0 + p * kRows) {
+      have |= 1u << p;
+    } else {
+      v[p] = make_uint4(0, 0, 0, 0);
+      astray = astray || at[p] >= 0;
+    }
   }
+  if (astray) record_status(SVDQ_ERR_INVALID_ARG);
   float amax = 0.0f;
 #pragma unroll
   for (int p = 0; p < kPass; ++p) {

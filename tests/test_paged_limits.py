@@ -247,6 +247,78 @@ def test_every_bad_block_number_is_recorded(gpu, heads, kv, d, bs, new, lens, nu
     assert sv.get_status() == sv.OK
 
 
+# ------------------------------------------------------------ skipped tokens
+def appended(x, slots, cu, codes, scale, fmt):
+    """The rule for slot maps with tokens left out (-1): the block's new tokens, whatever lies between them, share one scale."""
+    codes, scale = codes.copy(), scale.copy()
+    bs = codes.shape[2]
+    for a, e in zip(cu[:-1], cu[1:]):
+        own = {}
+        for t in range(a, e):
+            if slots[t] >= 0:
+                own.setdefault(int(slots[t]) // bs, {})[int(slots[t]) % bs] = t
+        for blk, rows in own.items():
+            lo, hi = min(rows), max(rows) + 1
+            part = np.zeros((hi - lo, *x.shape[1:]))
+            for r, t in rows.items():
+                part[r - lo] = x[t]
+            kept = codes[blk].copy()
+            codes, scale = pk.append(part, np.arange(blk * bs + lo, blk * bs + hi), [0, hi - lo], codes, scale, fmt)
+            for r in set(range(lo, hi)) - set(rows):
+                codes[blk, :, r] = kept[:, r]
+    return codes, scale
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("d,bs", [(64, 16), (128, 16), (64, 128), (128, 64)])
+@pytest.mark.parametrize("skip", ["leading", "block starts", "first blocks", "scattered", "all but the last", "all"])
+def test_append_leaves_skipped_tokens_out(gpu, fmt, d, bs, skip):
+    """Slots of -1 anywhere in a request (a prefix that is cached already, tokens of no interest): those tokens and no
+    others are left out."""
+    r, kv = random.Random(bs + d), 2
+    olds, news = [0, 5, bs - 1, 2 * bs + 3], [3 * bs + 2, 2 * bs, bs + 4, 1]
+    lens = [a + b for a, b in zip(olds, news)]
+    P = Pool(bs + d, kv, kv, d, bs, sum(-(-L // bs) for L in lens) + 3, fmt, "bf16")
+    table = make_table(P.rng, lens, bs, P.n, max(-(-L // bs) for L in lens))
+    slots, cu = [], [0]
+    for i, (o, L) in enumerate(zip(olds, lens)):
+        for t in range(o, L):
+            out = {"leading": t < o + 3 and L > o + 1, "block starts": t % bs == 0, "first blocks": t < o + bs + 2, "scattered": r.random() < 0.4,
+                   "all but the last": t < L - 1, "all": True}[skip]
+            slots.append(-1 if out else int(table[i, t // bs]) * bs + t % bs)
+        cu.append(len(slots))
+    slots = np.array(slots, np.int32)
+    x = (normal(P.rng, len(slots), 2 * kv * d) * 3).to(dtype_of("bf16"))
+    x64 = x.double().numpy()
+    want = [appended(x64[:, k * kv * d:(k + 1) * kv * d].reshape(-1, kv, d), slots, cu, P.codes[k], P.scale[k], fmt) for k in (0, 1)]
+    c, xd = P.to_device(), x.cuda()
+    b = sv.paged_batch(dev(table), dev(np.array(lens, np.int32)), dev(np.array(cu, np.int32)), dev(slots), max_new=max(news), max_len=max(lens))
+    sv.paged_append(c, b, xd[:, :kv * d], xd[:, kv * d:])
+    for k in (0, 1):
+        assert np.array_equal(P.t[2 * k + 1].cpu().numpy(), want[k][1])
+        assert np.array_equal(P.t[2 * k].cpu().numpy(), want[k][0])
+    assert sv.get_status() == sv.OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("slots", [[0, 1, 3, 2], [3, 3, 5, 6], [0, 1, 34, 3], [5, 6, 7, 20], [-1, 4, 9, 6]])
+def test_append_records_tokens_astray(gpu, slots):
+    """Slots of one request that do not follow one another in their block, the same slot twice, another block's slot:
+    left out, recorded, and the tokens in place are written."""
+    P = Pool(9, 2, 2, 64, 16, 4, "int8", "bf16")
+    x = (normal(P.rng, 4, 128) * 30).to(dtype_of("bf16"))
+    lead = next(k for k, v in enumerate(slots) if v >= 0)
+    place = np.array([v if v == slots[lead] + k - lead else -1 for k, v in enumerate(slots)], np.int32)
+    want = appended(x.double().numpy().reshape(4, 2, 64), place, [0, 4], P.codes[0], P.scale[0], "int8")
+    c, xd = P.to_device(), x.cuda()
+    b = sv.paged_batch(dev(np.zeros((1, 4), np.int32)), dev(np.zeros(1, np.int32)), dev(np.array([0, 4], np.int32)), dev(np.array(slots, np.int32)),
+                       max_new=4, max_len=64)
+    sv.paged_append(c, b, xd, xd)
+    assert np.array_equal(P.t[1].cpu().numpy(), want[1]) and np.array_equal(P.t[0].cpu().numpy(), want[0])
+    assert sv.get_status() == sv.ERR_INVALID_ARG and sv.get_status() == sv.OK
+
+
 # ------------------------------------------------------------- the schedule's size
 def test_the_schedule_has_as_many_parts_as_are_resident():
     """9 to 16 rows of 64 values: three CTAs of the balanced schedule fit an SM (168 registers a thread of 128), not four."""
