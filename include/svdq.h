@@ -275,7 +275,7 @@ typedef struct svdq_paged_batch {
 
 /*
  * The plan of a step: request i's cached length goes from prev[i] to target[i]
- * (device, B int32 each).  Growing takes blocks off the front of the ring of
+ * (device, B int32 each; all arrays here 4-byte aligned).  Growing takes blocks off the front of the ring of
  * free block numbers (in request order), shrinking or ending (target 0) gives
  * the blocks above ceil(target / block_size) back to its end.
  *   ring       n_blocks int32; the free ones are ring[(head + k) % n_blocks],
@@ -292,7 +292,8 @@ typedef struct svdq_paged_batch {
  * for one request or n_tokens for all, head or count outside the ring, count and
  * the blocks given back together above n_blocks): no block moves, b->lens = prev,
  * b->cu = 0, b->slots = -1.
- * One kernel.  Errors: SVDQ_ERR_INVALID_ARG, SVDQ_ERR_UNSUPPORTED, SVDQ_ERR_CUDA.
+ * One kernel.  Errors: SVDQ_ERR_INVALID_ARG, SVDQ_ERR_ALIGNMENT, SVDQ_ERR_UNSUPPORTED,
+ * SVDQ_ERR_CUDA.
  */
 svdq_status svdq_paged_plan(const svdq_paged_batch* b, int32_t block_size, int32_t n_blocks, const int32_t* prev,
                             const int32_t* target, int32_t* ring, const int32_t* state_in, int32_t* state_out,

@@ -2042,6 +2042,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnA
 
 // ------------------------------------------------------------- host launchers
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// int32 arrays: a word that lies across words would end the CUDA context
+template <class... P>
+bool aligned4(const P*... p) { return ((reinterpret_cast<uintptr_t>(p) | ...) & 3) == 0; }
 
 int log2_block(int bs) {
   switch (bs) {
@@ -2287,6 +2290,7 @@ svdq_status svdq_paged_plan(const svdq_paged_batch* b, int32_t block_size, int32
     return SVDQ_ERR_INVALID_ARG;
   if ((int64_t)n_blocks * block_size > INT32_MAX) return SVDQ_ERR_UNSUPPORTED;
   if (state_in == state_out || prev == b->lens || target == b->lens) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned4(b->table, b->lens, b->cu, b->slots, prev, target, ring, state_in, state_out)) return SVDQ_ERR_ALIGNMENT;
   int sms = 0;
   if ((st = device_ready(&sms)) != SVDQ_OK) return st;
   PlanArgs A;
@@ -2310,7 +2314,7 @@ svdq_status svdq_paged_append(const svdq_paged_cache* c, const svdq_paged_batch*
   if (!K || !V || !b->cu || !b->slots) return SVDQ_ERR_INVALID_ARG;
   const int64_t row = (int64_t)c->kv_heads * c->head_dim;
   if (k_stride < row || v_stride < row) return SVDQ_ERR_INVALID_ARG;
-  if (!aligned16(K) || !aligned16(V) || k_stride % 8 != 0 || v_stride % 8 != 0) return SVDQ_ERR_ALIGNMENT;
+  if (!aligned16(K) || !aligned16(V) || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned4(b->cu, b->slots)) return SVDQ_ERR_ALIGNMENT;
   int sms = 0;
   if ((st = device_ready(&sms)) != SVDQ_OK) return st;
   AppendArgs A;
@@ -2343,7 +2347,8 @@ svdq_status svdq_paged_attention(const svdq_paged_cache* c, const svdq_paged_bat
   const int64_t row = (int64_t)c->heads * c->head_dim;
   if (q_stride < row || out_stride < row) return SVDQ_ERR_INVALID_ARG;
   if (ws_bytes < attention_ws(c, b)) return SVDQ_ERR_WORKSPACE;
-  if (!aligned16(Q) || !aligned16(out) || !aligned16(workspace) || q_stride % 8 != 0 || out_stride % 8 != 0)
+  if (!aligned16(Q) || !aligned16(out) || !aligned16(workspace) || q_stride % 8 != 0 || out_stride % 8 != 0 ||
+      !aligned4(b->table, b->lens, b->cu))
     return SVDQ_ERR_ALIGNMENT;
   int sms = 0;
   if ((st = device_ready(&sms)) != SVDQ_OK) return st;

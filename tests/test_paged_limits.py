@@ -7,7 +7,7 @@ import pytest
 
 import rank_gemm_svdq_b200 as sv
 from oracle import pagedkv as pk
-from tests.test_paged import UNIT, Pool, dev, dtype_of, make_table
+from tests.test_paged import UNIT, Pool, call_append, call_attend, call_plan, dev, dtype_of, make_table, raw_batch, raw_cache
 
 
 def both(P, q, new, lens, table, causal=True, dtype="bf16", scale=None, max_new=None):
@@ -317,6 +317,22 @@ def test_append_records_tokens_astray(gpu, slots):
     sv.paged_append(c, b, xd, xd)
     assert np.array_equal(P.t[1].cpu().numpy(), want[1]) and np.array_equal(P.t[0].cpu().numpy(), want[0])
     assert sv.get_status() == sv.ERR_INVALID_ARG and sv.get_status() == sv.OK
+
+
+# -------------------------------------------------------------- bad pointers
+def test_unaligned_int32_arrays_refused():
+    """Addresses between two int32 words never reach a launch."""
+    A, c = sv.ERR_ALIGNMENT, raw_cache()
+    for name in ("table", "lens", "cu", "slots"):
+        for off in (1, 2, 3):
+            b = raw_batch(**{"lens": 12288, name: 20480 + off})
+            assert call_plan(b) == A, name
+            if name in ("cu", "slots"):
+                assert call_append(c, b) == A, name
+            if name != "slots":
+                assert call_attend(c, b) == A, name
+    for name in ("prev", "target", "ring", "sin", "sout"):
+        assert call_plan(raw_batch(lens=12288), **{name: 20482}) == A, name
 
 
 # ------------------------------------------------------------- the schedule's size
