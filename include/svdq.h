@@ -26,8 +26,9 @@
  *   bias  N fp32 or NULL (zero bias); host memory.
  *
  * Ownership: the caller allocates and owns every buffer (host and device).
- * The library allocates no device memory and keeps no per-call state; one
- * device-global status word per GPU records device-side failures.
+ * The library allocates no device memory and keeps no per-call state; a
+ * device-global status word per GPU (and one more for the paged cache) records
+ * device-side failures.
  *
  * Errors: every function returns an svdq_status and never aborts.  Device
  * work is launched asynchronously; failures inside a kernel (a bounded wait
@@ -427,7 +428,8 @@ svdq_status svdq_gemm_chain(const svdq_params* p, const void* blob_dev, int64_t 
 svdq_status svdq_export_act(const svdq_params* p, const void* workspace, int64_t M,
                             uint8_t* codes, void* scales, float* u, svdq_stream stream);
 
-/* Synchronise `stream`, read and clear this device's status word. */
+/* Synchronise `stream`, read and clear this device's status word (the paged cache's
+ * kernels have one of their own: where both hold a failure, the next call returns the second). */
 svdq_status svdq_get_status(svdq_stream stream);
 
 const char* svdq_status_string(svdq_status s);

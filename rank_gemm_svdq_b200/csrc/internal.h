@@ -11,7 +11,7 @@ namespace svdq {
 svdq_status cuda_failure(cudaError_t e, const char* where);
 
 // Read and clear the status word of the paged-cache kernels (each translation
-// unit of kernels has its own word; svdq_get_status reads them all).
+// unit of kernels has its own word; svdq_get_status reads this one when the other is clear).
 cudaError_t paged_status_take(unsigned int* v);
 
 }  // namespace svdq

@@ -2263,7 +2263,12 @@ struct AttnCall {
 }  // namespace paged
 
 cudaError_t paged_status_take(unsigned int* v) {
-  cudaError_t e = cudaMemcpyFromSymbol(v, dev::g_status, sizeof(*v));
+  *v = 0;
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  // no call of the paged cache got as far as a launch on this device: nothing to read (a copy costs microseconds)
+  if (e != cudaSuccess || device < 0 || device >= 64 || paged::g_devices[device].state.load(std::memory_order_acquire) != 1) return e;
+  e = cudaMemcpyFromSymbol(v, dev::g_status, sizeof(*v));
   if (e == cudaSuccess && *v != 0) {
     const unsigned int z = 0;
     e = cudaMemcpyToSymbol(dev::g_status, &z, sizeof(z));

@@ -2877,11 +2877,11 @@ svdq_status svdq_get_status(svdq_stream stream) {
     const unsigned int z = 0;
     e = cudaMemcpyToSymbol(dev::g_status, &z, sizeof(z));
     if (e != cudaSuccess) return cuda_fail(e, "svdq_get_status clear");
+    return (svdq_status)v;                 // the paged cache's word, if it holds one too, is the next call's
   }
-  unsigned int w = 0;
-  e = paged_status_take(&w);
+  e = paged_status_take(&v);
   if (e != cudaSuccess) return cuda_fail(e, "svdq_get_status (paged cache)");
-  return (svdq_status)(v != 0 ? v : w);
+  return (svdq_status)v;
 }
 
 const char* svdq_last_error_string(void) { return g_last_error; }

@@ -335,6 +335,18 @@ def test_unaligned_int32_arrays_refused():
         assert call_plan(raw_batch(lens=12288), **{name: 20482}) == A, name
 
 
+# ------------------------------------------------------------- recorded failures
+@pytest.mark.gpu
+def test_two_recorded_failures_are_both_read(gpu):
+    """A wait that ran out in the layer's kernels and a bad block number in the paged cache's: one after the other."""
+    P, table = pool(3, 2, 2, 64, 16, [40], "int8", "bf16")
+    table[0, 1] = -1
+    assert sv.get_status() == sv.OK
+    sv.probe_timeout(1_000_000)
+    both(P, normal(P.rng, 1, 128), [1], [40], table)
+    assert sv.get_status() == sv.ERR_TIMEOUT and sv.get_status() == sv.ERR_INVALID_ARG and sv.get_status() == sv.OK
+
+
 # ------------------------------------------------------------- the schedule's size
 def test_the_schedule_has_as_many_parts_as_are_resident():
     """9 to 16 rows of 64 values: three CTAs of the balanced schedule fit an SM (168 registers a thread of 128), not four."""
