@@ -308,7 +308,9 @@ svdq_status svdq_paged_plan(const svdq_paged_batch* b, int32_t block_size, int32
  *   s = max(s_old, max |x| / qmax)   (qmax 127 or 448; s_old = 0 in a block
  *                                     whose first row is new)
  *   code = round(x / s);  earlier rows, when s grew: code = round(code (s_old / s)).
- * A block of zeros has s = 0.  Inputs finite.
+ * A block of zeros has s = 0.  A NaN or an infinity gives its block and head the
+ * scale +infinity, which is recorded for svdq_get_status (SVDQ_ERR_INVALID_ARG): attention
+ * rows that see that block come out as NaN or infinite, others are as before.
  * Slots: a token whose slot is -1 is left out, wherever in the request it stands (a
  * prefix that is cached already).  The others lie as the plan puts them: token k of a request
  * in row (row of its token 0 + k) mod block_size, block after block, and a block

@@ -217,6 +217,13 @@ template <> struct Fmt<SVDQ_KV_INT8> { static constexpr float qmax = 127.0f; };
 template <> struct Fmt<SVDQ_KV_E4M3> { static constexpr float qmax = 448.0f; };
 
 template <int DT>
+__device__ __forceinline__ float load16(uint16_t h) {
+  if constexpr (DT == SVDQ_BF16) return __uint_as_float((uint32_t)h << 16);
+  else return __half2float(__ushort_as_half(h));
+}
+template <int DT> constexpr uint32_t kInf16 = DT == SVDQ_BF16 ? 0x7F80u : 0x7C00u;   // bits of +infinity
+
+template <int DT>
 __device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -301,7 +308,7 @@ template <int DT, int FMT, int D, int LB>
 __global__ void __launch_bounds__(append_threads(1 << LB, D), 768 / append_threads(1 << LB, D)) paged_append_kernel(const AppendArgs A) {
   constexpr int kAppendThreads = append_threads(1 << LB, D);
   constexpr int BS = 1 << LB, kPerRow = D / 8, kRows = kAppendThreads / kPerRow, kPass = BS / kRows > 0 ? BS / kRows : 1;
-  __shared__ float s_amax[kAppendThreads / 32];
+  __shared__ uint32_t s_top[kAppendThreads / 32];
   const int tid = threadIdx.x, w = blockIdx.x, h = blockIdx.y, which = blockIdx.z;
   griddep_wait();
   griddep_launch();
@@ -374,20 +381,25 @@ __global__ void __launch_bounds__(append_threads(1 << LB, D), 768 / append_threa
     }
   }
   if (astray) record_status(SVDQ_ERR_INVALID_ARG);
-  float amax = 0.0f;
+  // the largest magnitude by its bits, two values at once: as whole numbers they order like the magnitudes, with
+  // infinity and then NaN above all others, where a maximum of floats would let a NaN vanish
+  uint32_t top = 0;
 #pragma unroll
   for (int p = 0; p < kPass; ++p) {
-    float f[8];
-    unpack8<DT>(v[p], f);
+    const uint32_t u[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
+    for (int k = 0; k < 4; ++k) top = __vmaxu2(top, u[k] & 0x7FFF7FFFu);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((tid & 31) == 0) s_amax[tid >> 5] = amax;
+  top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xFFFFu));
+  if ((tid & 31) == 0) s_top[tid >> 5] = top;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kAppendThreads / 32; ++k) amax = fmaxf(amax, s_amax[k]);
+  for (int k = 0; k < kAppendThreads / 32; ++k) top = max(top, s_top[k]);
+  float amax = load16<DT>((uint16_t)top);
+  if (top >= kInf16<DT>) {                              // the scale says so to every reader: what sees the block is NaN
+    amax = INFINITY;
+    if (tid == 0) record_status(SVDQ_ERR_INVALID_ARG);
+  }
   const float s = fmaxf(s_old, __fdiv_rn(amax, Fmt<FMT>::qmax));
   uint8_t* base = (which ? A.codes[1] : A.codes[0]) + cell * (size_t)(BS * D);
   if (s > s_old) {
@@ -427,10 +439,10 @@ __global__ void __launch_bounds__(append_threads(1 << LB, D), 768 / append_threa
   if (s >= 0x1p-60f && s <= 0x1p+60f) {
     const float rs = __frcp_rn(s);
     write([&](float x) { return quotient(x, s, rs); });
-  } else if (s > 0.0f) {
+  } else if (s > 0.0f && s < INFINITY) {
     write([&](float x) { return divide_rn(x, s); });
   } else {
-    write([](float) { return 0.0f; });
+    write([](float) { return 0.0f; });                  // zeros; or 0 times an infinite scale, which no reader mistakes
   }
 }
 
@@ -495,11 +507,6 @@ __device__ __forceinline__ int seen_by(const AttnArgs& A, const Rows& R, int r) 
   return A.causal ? max(0, R.L - R.n + r / A.G + 1) : R.L;
 }
 
-template <int DT>
-__device__ __forceinline__ float load16(uint16_t h) {
-  if constexpr (DT == SVDQ_BF16) return __uint_as_float((uint32_t)h << 16);
-  else return __half2float(__ushort_as_half(h));
-}
 template <int DT>
 __device__ __forceinline__ uint16_t store16(float f) {
   if constexpr (DT == SVDQ_BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(f));
@@ -1781,7 +1788,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
 #pragma unroll
         for (int q = 0; q < H; ++q) store_codes<FMT>(sk + st * TB, 32 * w + r4 + 8 * i, q, c, kr[i * H + q]);
       if ((lane & 15) == 0)
-        meta[(t & (kTileMeta - 1)) * 8 + 2 * w + (lane >> 4)] = TileMeta{g_sk, g_sv > 0.0f ? log2f(g_sv) : -INFINITY, g_gone, 0};
+        meta[(t & (kTileMeta - 1)) * 8 + 2 * w + (lane >> 4)] = TileMeta{g_sk, g_sv > 0.0f ? fminf(log2f(g_sv), FLT_MAX) : -INFINITY, g_gone, 0};   // an infinite scale: -inf + it stays -inf
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&k_full[st]);

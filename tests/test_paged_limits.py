@@ -228,6 +228,45 @@ def test_append_keeps_the_sign_of_zero(gpu, fmt, size):
     assert np.array_equal(P.t[0].cpu().numpy(), want[0]) and np.array_equal(P.t[1].cpu().numpy(), want[1])
 
 
+# ------------------------------------------------------- NaN and infinities
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
+@pytest.mark.parametrize("fmt,dtype", BOTH_FORMATS)
+@pytest.mark.parametrize("bad,where", [(float("nan"), 0), (float("nan"), 1), (float("-inf"), 0), (float("inf"), 1)])
+def test_non_finite_values_are_seen(gpu, heads, kv, d, bs, new, lens, fmt, dtype, bad, where):
+    """One NaN or infinity in a token's keys or values: recorded, and not finite for the rows that see its block in its
+    head.  All other rows have the bits that they have with a finite value there."""
+    import torch
+    P, table = pool(sum(lens) + 6, heads, kv, d, bs, lens, fmt, dtype)
+    n, G, L = sum(new), heads // kv, lens[0]
+    q = normal(P.rng, n, heads * d, dtype).to(dtype_of(dtype)).cuda()
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    blk = int(table[0, (L - 1) // bs])
+    slot = dev(np.array([blk * bs + (L - 1) % bs], np.int32))
+    one = sv.paged_batch(dev(table[:1]), dev(np.array([L], np.int32)), dev(np.array([0, 1], np.int32)), slot, max_new=1, max_len=L)
+    b = sv.paged_batch(dev(table), dev(np.array(lens, np.int32)), dev(cu), None, n_tokens=n, max_new=max(new), max_len=max(lens))
+    kv_new = normal(P.rng, 2, kv * d, dtype).to(dtype_of(dtype))
+    out = []
+    for value in (1.0, bad):
+        c = P.to_device()
+        kv_new[where, 5] = value                           # in head 0
+        x = kv_new.cuda()
+        sv.paged_append(c, one, x[:1], x[1:])
+        assert sv.get_status() == (sv.OK if value == 1.0 else sv.ERR_INVALID_ARG)
+        if value != 1.0:
+            assert torch.isinf(P.t[2 * where + 1][blk, 0]) and torch.isfinite(P.t[2 * where + 1][blk, 1:]).all()
+        ws = torch.empty(sv.paged_attention_workspace_bytes(c, b), dtype=torch.uint8, device="cuda")
+        o = torch.zeros(n, heads * d, dtype=dtype_of(dtype), device="cuda")
+        sv.paged_attention(c, b, q, o, ws)
+        out.append(o.cpu().view(n, heads, d))
+    sees = torch.zeros(n, heads, dtype=torch.bool)
+    for j in range(new[0]):
+        sees[j, :G] = L - new[0] + j + 1 > (L - 1) // bs * bs
+    assert torch.isfinite(out[0].float()).all() and not torch.isfinite(out[1][sees].float()).any()
+    assert torch.equal(out[0][~sees], out[1][~sees]) and sees.any() and (~sees).any()
+    assert sv.get_status() == sv.OK
+
+
 # --------------------------------------------------------------- bad pages
 @pytest.mark.gpu
 @pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
