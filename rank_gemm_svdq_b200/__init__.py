@@ -366,7 +366,7 @@ def _rows16(t, n: int, cols: int, cache: svdq_paged_cache, name: str) -> tuple[i
     if not ok or shape[0] < n:
         raise SVDQError(ERR_INVALID_ARG, f"{name}: {n} rows of {cols} values in the cache's dtype and on its device, "
                                          "contiguous within a row")
-    return t.data_ptr(), stride if shape[0] > 1 else max(cols, stride)
+    return t.data_ptr(), stride if shape[0] > 1 else cols   # a single row's stride says nothing
 
 
 def paged_append(cache: svdq_paged_cache, batch: svdq_paged_batch, K, V, stream=None):

@@ -374,6 +374,19 @@ def test_unaligned_int32_arrays_refused():
         assert call_plan(raw_batch(lens=12288), **{name: 20482}) == A, name
 
 
+def test_one_row_of_any_stride_is_taken():
+    """The stride of a single row says nothing: a view of a wider, oddly sized row keeps its row."""
+    import torch
+    z = lambda *s, t=torch.int32: torch.zeros(*s, dtype=t)  # noqa: E731
+    codes, scale = z(4 * 2 * 16 * 64, t=torch.uint8), z(8, t=torch.float32)
+    c = sv.paged_cache(4, 2, 64, 16, 4, "int8", "bf16", codes, scale, codes, scale)
+    for wide in (128, 131, 4099):
+        x = z(3, wide, t=torch.bfloat16)
+        for row in (x[:1, :128], x[:1, :128].unflatten(1, (2, 64)), torch.as_strided(x, (1, 128), (1, 1))):
+            assert sv._rows16(row, 1, 128, c, "K") == (x.data_ptr(), 128)
+    assert sv._rows16(z(3, 136, t=torch.bfloat16)[:, :128], 3, 128, c, "K")[1] == 136
+
+
 # ------------------------------------------------------------- recorded failures
 @pytest.mark.gpu
 def test_two_recorded_failures_are_both_read(gpu):
