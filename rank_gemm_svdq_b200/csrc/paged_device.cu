@@ -475,7 +475,7 @@ struct AttnArgs {
   float* part_ml;          // [CTA][2][rows][2]
   struct Piece* pieces;    // [CTA][2]
   int64_t q_stride, out_stride;
-  int B, max_blocks, n_tokens, max_new, max_len, n_blocks, heads, kv, G, lb, causal, splits;
+  int B, max_blocks, n_tokens, max_new, max_len, n_blocks, kv, G, lb, causal, splits;
   float scale_log2;
   double inv_parts;        // 1 / CTAs of the schedule
   int snap;                // items are not cut
@@ -2378,7 +2378,7 @@ svdq_status svdq_paged_attention(const svdq_paged_cache* c, const svdq_paged_bat
   }
   A.q_stride = q_stride; A.out_stride = out_stride;
   A.B = b->B; A.max_blocks = b->max_blocks; A.n_tokens = b->n_tokens; A.max_new = b->max_new; A.max_len = b->max_len;
-  A.n_blocks = c->n_blocks; A.heads = c->heads; A.kv = c->kv_heads; A.G = c->heads / c->kv_heads;
+  A.n_blocks = c->n_blocks; A.kv = c->kv_heads; A.G = c->heads / c->kv_heads;
   A.lb = log2_block(c->block_size); A.causal = causal; A.splits = sp.ctas; A.snap = sp.snap;
   A.scale_log2 = scale * 1.4426950408889634f;
   A.inv_parts = 1.0 / sp.ctas;

@@ -387,6 +387,74 @@ def test_one_row_of_any_stride_is_taken():
     assert sv._rows16(z(3, 136, t=torch.bfloat16)[:, :128], 3, 128, c, "K")[1] == 136
 
 
+# ---------------------------------------------------------- many requests
+@pytest.mark.gpu
+def test_plan_of_16384_requests(gpu):
+    """The largest batch: 32 rounds of the scan, and all of the shared memory that it may take."""
+    import torch
+    B, bs, mb, cap = 16384, 16, 3, 40000
+    r = random.Random(8)
+    n_blocks = B * mb
+    table, ring, head, count = np.zeros((B, mb), np.int32), np.arange(n_blocks, dtype=np.int32), 0, n_blocks
+    lens = [0] * B
+    t = dict(table=dev(table), ring=dev(ring), lens=torch.zeros(B, dtype=torch.int32).cuda(), cu=torch.zeros(B + 1, dtype=torch.int32).cuda(),
+             slots=torch.zeros(cap, dtype=torch.int32).cuda())
+    b = sv.paged_batch(t["table"], t["lens"], t["cu"], t["slots"], max_new=30, max_len=mb * bs)
+    for step in range(3):
+        target = [0 if r.random() < 0.1 else min(mb * bs, n + (r.randint(1, 30) if r.random() < 0.1 else 1)) for n in lens]
+        want = pk.plan(lens, target, table, ring, head, count, bs, cap, 30, mb * bs)
+        assert want["state"][2] == 0
+        sout = torch.zeros(4, dtype=torch.int32).cuda()
+        sv.paged_plan(b, bs, dev(np.array(lens, np.int32)), dev(np.array(target, np.int32)), t["ring"],
+                      dev(np.array([head, count, 0, 0], np.int32)), sout)
+        for name in t:
+            assert np.array_equal(t[name].cpu().numpy(), want[name]), (step, name)
+        assert np.array_equal(sout.cpu().numpy(), want["state"])
+        table, ring, lens = want["table"], want["ring"], want["lens"].tolist()
+        head, count = int(want["state"][0]), int(want["state"][1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("most", [1, 40])
+@pytest.mark.parametrize("d,bs", [(64, 16), (128, 128)])
+def test_append_of_many_requests(gpu, most, d, bs):
+    """More requests than a pass of the search for a work item's request takes, some without a new token."""
+    r, B, kv = random.Random(most), 700, 1
+    news = [0 if r.random() < 0.2 else r.randint(1, most) for _ in range(B)]
+    olds = [r.randint(0, 2 * bs) for _ in range(B)]
+    lens = [a + b for a, b in zip(olds, news)]
+    P = Pool(most + d, kv, kv, d, bs, sum(-(-L // bs) for L in lens) + 1, "int8", "bf16")
+    table = make_table(P.rng, lens, bs, P.n, max(-(-L // bs) for L in lens))
+    slots, cu = [], [0]
+    for i, (o, L) in enumerate(zip(olds, lens)):
+        slots += [int(table[i, t // bs]) * bs + t % bs for t in range(o, L)]
+        cu.append(len(slots))
+    x = normal(P.rng, len(slots), 2 * kv * d).to(dtype_of("bf16"))
+    want = [pk.append(x[:, k * d:(k + 1) * d].double().numpy().reshape(-1, 1, d), slots, cu, P.codes[k], P.scale[k], "int8") for k in (0, 1)]
+    c, xd = P.to_device(), x.cuda()
+    b = sv.paged_batch(dev(table), dev(np.array(lens, np.int32)), dev(np.array(cu, np.int32)), dev(np.array(slots, np.int32)), max_new=most,
+                       max_len=max(lens))
+    sv.paged_append(c, b, xd[:, :d], xd[:, d:])
+    for k in (0, 1):
+        assert np.array_equal(P.t[2 * k + 1].cpu().numpy(), want[k][1]) and np.array_equal(P.t[2 * k].cpu().numpy(), want[k][0])
+    assert sv.get_status() == sv.OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,most", [(1, 1, 30), (2, 1, 1), (8, 2, 5)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_of_many_requests(gpu, heads, kv, most, causal):
+    """More requests than a pass of the schedule's scan takes (128 or 512 threads), some without a query."""
+    r, B = random.Random(most), 1300
+    new = [0 if r.random() < 0.2 else r.randint(1, most) for _ in range(B)]
+    new[0] = most
+    lens = [r.randint(1, 90) + m for m in new]
+    P, table = pool(most, heads, kv, 64, 16, lens, "int8", "bf16")
+    _, got, want, tol = both(P, normal(P.rng, sum(new), heads * 64), new, lens, table, causal)
+    within(got, want, tol)
+    assert sv.get_status() == sv.OK
+
+
 # ------------------------------------------------------------- recorded failures
 @pytest.mark.gpu
 def test_two_recorded_failures_are_both_read(gpu):
