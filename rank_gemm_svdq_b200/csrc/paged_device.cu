@@ -557,9 +557,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// At least log2 s, at most one more; -120 for smaller s (so that 2^(m - n) is an fp32 number).
+// At least log2 s, at most one more; within [-120, 118], so that 2^(m - n) is a normal fp32 number.  A value scale
+// comes to 2^121 at most (the largest bf16 number over 127), and a weight so to 2^10.
 __device__ __forceinline__ float scale_exponent(float s) {
-  return fmaxf(__uint_as_float(0x4B000000u | (__float_as_uint(s) >> 23)) - 8388734.0f, -120.0f);   // 2^23 + field - (2^23 + 126)
+  return fminf(fmaxf(__uint_as_float(0x4B000000u | (__float_as_uint(s) >> 23)) - 8388734.0f, -120.0f), 118.0f);   // 2^23 + field - (2^23 + 126)
 }
 
 // A row's accumulator in units of 2^n to its result, 2^(n - m) / l, as two factors that neither over- nor underflow.
@@ -771,7 +772,7 @@ struct RowState {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const float z0 = m[nb][0] == -INFINITY ? 0.0f : m[nb][0], z1 = m[nb][1] == -INFINITY ? 0.0f : m[nb][1];
-      // m - n <= 127: where m was set, n became at least m - 120 - kGrow
+      // -125 <= m - n <= 127: n is at most a score (m + kGrow) plus 118; where m was set, n became at least m - 120 - kGrow
       const float rel0 = ex2(fminf(z0 - n[nb][0], 127.0f)), rel1 = ex2(fminf(z1 - n[nb][1], 127.0f));
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {

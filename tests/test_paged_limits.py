@@ -196,15 +196,26 @@ def test_values_of_subnormal_size(gpu, heads, kv, d, bs, new, lens, fmt, where):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
-def test_values_near_the_largest(gpu, heads, kv, d, bs, new, lens):
-    """Values up to 2^126 and uniform weights: a mean of finite values is finite."""
+@pytest.mark.parametrize("largest,growing", [(2.0 ** 126, False), (2.0 ** 128 - 2.0 ** 120, False), (2.0 ** 128 - 2.0 ** 120, True)])
+def test_values_near_the_largest(gpu, heads, kv, d, bs, new, lens, largest, growing):
+    """Values up to the largest bf16 number: a mean of finite values is finite.  Uniform weights, or scores that
+    grow by less than a reference may lag, to blocks of values 2^10 larger than the first ones."""
     P, table = pool(sum(lens) + 4, heads, kv, d, bs, lens, "int8", "bf16")
     P.codes[1] = np.abs(P.codes[1].view(np.int8)).view(np.uint8)
-    P.scale[1] = np.float32(2.0 ** 119)
+    P.scale[1] = np.float32(largest / 127)
     P.scale[0] *= np.float32(2.0 ** -20)
-    _, got, want, tol = both(P, normal(P.rng, sum(new), heads * d), new, lens, table)
+    q = normal(P.rng, sum(new), heads * d)
+    if growing:                                            # scores of 0 in the first two blocks, then of 4 (5.8 in log2)
+        q = q.abs() * 0 + 1
+        P.codes[0] = 127
+        P.scale[0] = 4.0 / (d ** 0.5 * 127.0)
+        for i in range(len(lens)):
+            P.scale[0, table[i, :2]] = 0.0
+            P.scale[1, table[i, :2]] *= np.float32(2.0 ** -10)
+    _, got, want, tol = both(P, q, new, lens, table)
     within(got, want, tol)
-    assert np.abs(got).max() > 2.0 ** 120
+    # 2^126 / 8 at least; where a request has no third block, all values are 2^10 smaller
+    assert np.abs(got).max() > (2.0 ** 115 if growing else 2.0 ** 123)
 
 
 @pytest.mark.gpu
