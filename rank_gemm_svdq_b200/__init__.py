@@ -313,6 +313,7 @@ def paged_cache(heads: int, kv_heads: int, head_dim: int, block_size: int, n_blo
                 kcodes, kscale, vcodes, vscale) -> svdq_paged_cache:
     """The pool of a paged 8-bit KV cache over the caller's device buffers: codes n_blocks x kv_heads x
     block_size x head_dim bytes, scales n_blocks x kv_heads fp32.  Keeps the tensors alive."""
+    import torch
     c = svdq_paged_cache(None, None, None, None, heads, kv_heads, head_dim, block_size, n_blocks, KV_FMT[fmt],
                          DTYPE[dtype], 0)
     cells, c.device = n_blocks * kv_heads, kcodes.get_device()
@@ -320,6 +321,7 @@ def paged_cache(heads: int, kv_heads: int, head_dim: int, block_size: int, n_blo
                        ("kscale", kscale, 4 * cells), ("vscale", vscale, 4 * cells)):
         _expect(t.is_contiguous() and t.numel() * t.element_size() >= n, f"paged_cache: {name}, contiguous, {n} bytes")
         _expect(t.get_device() == c.device, f"paged_cache: {name} on device {c.device}")
+        _expect(name in ("kcodes", "vcodes") or t.dtype is torch.float32, f"paged_cache: {name} in float32")
         setattr(c, name, t.data_ptr())
     c.tensors, c.ref = (kcodes, kscale, vcodes, vscale), ctypes.addressof(c)
     c.q_cols, c.kv_cols = heads * head_dim, kv_heads * head_dim

@@ -385,6 +385,19 @@ def test_unaligned_int32_arrays_refused():
         assert call_plan(raw_batch(lens=12288), **{name: 20482}) == A, name
 
 
+def test_scales_of_another_type_refused():
+    """Scales are fp32; a buffer of another type with as many bytes would be read as something else."""
+    import torch
+    codes = torch.zeros(4 * 2 * 16 * 64, dtype=torch.uint8)
+    ok = torch.zeros(8, dtype=torch.float32)
+    for dtype, n in ((torch.float64, 8), (torch.float16, 16), (torch.bfloat16, 16), (torch.int32, 8), (torch.float32, 7)):
+        bad = torch.zeros(n, dtype=dtype)
+        for args in ((codes, bad, codes, ok), (codes, ok, codes, bad)):
+            with pytest.raises(sv.SVDQError):
+                sv.paged_cache(4, 2, 64, 16, 4, "int8", "bf16", *args)
+    sv.paged_cache(4, 2, 64, 16, 4, "int8", "bf16", codes, ok, codes, ok)
+
+
 def test_one_row_of_any_stride_is_taken():
     """The stride of a single row says nothing: a view of a wider, oddly sized row keeps its row."""
     import torch
