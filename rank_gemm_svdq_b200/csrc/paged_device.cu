@@ -1004,7 +1004,7 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
       ml[s].y *= ml[s].x == -INFINITY ? 0.0f : ex2(ml[s].x - M);
       L += ml[s].y;
     }
-    const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
+    const float inv = L > 0.0f ? __frcp_rn(L) : 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int s = 0; s < kMaxCluster; ++s) {
@@ -2019,7 +2019,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnA
         ml[b].y *= ml[b].x == -INFINITY ? 0.0f : ex2(ml[b].x - m);
         l += ml[b].y;
       }
-      const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+      const float inv = l > 0.0f ? __frcp_rn(l) : 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] *= old * inv;
 #pragma unroll
@@ -2042,7 +2042,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const AttnA
       const float own = part(make_float2(m, l));
       float all = own;
       for (int w = 1; w < wide; ++w) all += part(s_ml[warp + w]);
-      const float inv = all > 0.0f ? __fdiv_rn(1.0f, all) : 0.0f;
+      const float inv = all > 0.0f ? __frcp_rn(all) : 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] *= own * inv;
       for (int w = 1; w < wide; ++w) {
