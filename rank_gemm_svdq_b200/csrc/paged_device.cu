@@ -6,6 +6,10 @@
 // Block b of the pool holds, for every key/value head h, `bs` tokens of d 8-bit
 // codes (contiguous bs x d bytes at ((b kv + h) bs d)) and one fp32 scale for the
 // keys and one for the values (at b kv + h): x ~ code * scale.
+//
+// Times in comments: device time on one B200 in a CUDA graph of 20 calls, where what
+// fits the 126 MB L2 is read from it; "as a call" is a call among others from Python
+// with inputs that change from call to call.
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -41,8 +45,8 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // needs no communication between CTAs.  A token's block is found without reading
 // what another CTA writes: blocks below ceil(prev/bs) come from the table, later
 // ones from the ring.  Latency-bound: the lengths' load, the scan, one search.
-// 3.8 us for 64 decoding requests, 7.3 us for a mixed step of 1000, 6.7 us for 256
-// prompts of 570,000 slots (one slot at a time a thread: 9.2 us).
+// 3.8 us for 64 decoding requests, 7.6 us for a mixed step of 1000, 6.8 us for 256
+// prompts of 570,000 slots (one slot at a time a thread: 9.2 us); as calls 6.8, 7.6, 10.4.
 constexpr int kPlanThreads = 512, kPlanSlots = 4;
 
 struct PlanArgs {
@@ -207,9 +211,11 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
 // floor(cu_i / bs) + 2 i, which leaves it at least as many as it touches blocks
 // (<= floor(new / bs) + 2), so the grid needs only n_tokens and B on the host; + i
 // where no request has more than one new token.  Bound by the chain lengths -> slots
-// -> rows of each CTA, so by how many CTAs are resident: 80 registers, 24 warps an SM
-// (16 warps: 25.8 us, 32 with spills: 22.4 us).  Five prompts of 15,000 tokens, 8 heads
-// of 128: 21.9 us, 4.0 TB/s; 48 single tokens: 3.6 us.
+// -> rows of each CTA, so by how many CTAs are resident: at most 80 registers, 24 warps
+// an SM (at a time when a thread needed 80: 16 warps 25.8 us, 24 21.9, 32 with spills 22.4;
+// now 72 and no spills).  Five prompts of 15,000 tokens in all, 8 heads of 128: 21.7 us,
+// as a call 24.2 (3.6 TB/s); 48 single tokens 3.8 us, 1000 49 us (every CTA's search for
+// its request is linear in B).
 constexpr int append_threads(int BS, int D) { return BS * D >= 16384 ? 256 : 128; }
 
 template <int FMT> struct Fmt;
@@ -422,7 +428,7 @@ __global__ void __launch_bounds__(append_threads(1 << LB, D), 768 / append_threa
     scale[cell] = 0.0f;                     // a fresh block of zeros
   }
   // two copies of the loop: with the division inlined at every value the code left the
-  // instruction cache (five prompts of 15,000 tokens in all: 47 us, now 26 us)
+  // instruction cache (five prompts of 15,000 tokens in all: 47 us, without it 26)
   const auto write = [&](auto divide) {
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
@@ -613,7 +619,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs& A, const Rows& R, i
 // schedule (paged_flat_kernel).  The fragments are read straight from the codes: the order of the
 // contraction over d is free, so 16 bytes of a key row serve 4 k-steps, and 16 bytes
 // of four value rows the 16 values of d that a lane needs.  One request of 333 tokens, 32
-// heads: 7.6 us, a chain of loads (lengths, table, scales, codes) and two joins.
+// heads: 7.1 us, a chain of loads (lengths, table, scales, codes) and two joins.
 constexpr int kDecWarps = 4, kDecTile = 32, kDecStages = 2, kDecGroup = 32, kMaxCluster = 8;
 constexpr int dec_stage_bytes(int D) { return kDecTile * D * 2; }
 constexpr int dec_ring_bytes(int D) { return kDecWarps * kDecStages * dec_stage_bytes(D); }
@@ -1028,9 +1034,9 @@ __global__ void __launch_bounds__(kDecWarps * 32) paged_rows_kernel(const AttnAr
 // which sums in closed form over the row blocks r of a head, the heads and the
 // requests.  CTA c of N takes the costs [T c / N, T (c + 1) / N); a border inside an
 // item cuts its token tiles in proportion.  The two pieces of a cut item go to the
-// workspace and paged_join_kernel adds them; everything else is written directly.
-// Measured against a grid of (item, fixed split): six ragged prompts, whose rows see
-// 2 to 12 tiles, 283 -> 209 us; 256 equal items on 148 SMs took two full waves (782 -> 610 us).
+// workspace and paged_join_kernel joins them; everything else is written directly.
+// Measured against a grid of (item, fixed split) when it was brought in: six ragged prompts, whose
+// rows see 2 to 12 tiles, 283 -> 209 us; 256 equal items on 148 SMs took two full waves (782 -> 610 us).
 constexpr int kTileTok = 128, kTileRows = 256;
 struct Item {
   int req, h, a, n, L, rows, r0, lo, hi, out;              // token tiles [lo, hi); hi < 0: no more items
@@ -1169,9 +1175,11 @@ struct Walk {
 // takes the 32 tokens at 32 w of each 128-token tile.  Pieces of cut items go to the
 // workspace for paged_join_kernel; where A.snap is set items are not cut, and belong to
 // the CTA in whose share they start.  64 requests of up to 4096 tokens (346 MB of int8
-// codes): 72 us, 4.8 TB/s; one of 131071 (268 MB of E4M3): 56 us.  While it streams it
-// keeps up with HBM; the rest is the first chain of loads, 5 us, queries and the joins.
-// Tiles of 16 tokens in 16 warps an SM instead of 32 in 12: 89 and 62 us.
+// codes): 71.5 us, 4.8 TB/s; one of 131071 (268 MB of E4M3): 57 us.  Beyond HBM's rate it
+// pays the first chain of loads, 5 us, queries and joins, and bank conflicts: value rows of
+// 128 bytes are read four lanes to a bank, key rows two, over a quarter of the kernel's cycles
+// by the counter.  Tiles of 16 tokens in 16 warps an SM instead of 32 in 12: 89 and 62 us
+// (against 80 and 60 then).
 template <int D, int NB>
 struct FlatSmem {
   uint8_t ring[dec_ring_bytes(D)];
@@ -1375,16 +1383,17 @@ __global__ void __launch_bounds__(kDecWarps * 32, flat_per_sm(D, 8 * NB)) paged_
 // operand).  Roles:
 //   warps 0-3, 4-7   softmax of row tile 0 / 1, a row per thread: maximum, weights,
 //                    sum; rescales O only when the largest weighted magnitude grew
-//                    by more than 2^7; output
+//                    by more than 2^7; the next item's queries; output
 //   warps 8-11       codes -> fp16 (the next tile's codes already in registers)
-//                    of an item and, ahead of it, the queries of the next one
 //   warp 12          issues the MMAs: S0 S1 | P0V S0' | P1V S1' | ...
 //   warp 13          walks the schedule, up to eight items ahead
 // The value scale goes into a weight's exponent, p' = 2^(x + log2 s_v - n), so it costs
-// nothing per weight; the row sum takes each 16 tokens' sum times 2^(n - m) / s_v.  2048 rows x 32 heads
-// at 16384 tokens, d = 128: 610 us, 845 TFLOP/s.  Bound by the softmax warps, two a
-// scheduler: 3300 cycles a tile each where the exponentials alone take 1100.  144, 128
-// and 96 registers: a spilled value misses what is left of L1 and costs 600 cycles.
+// nothing per weight; the row sum takes each 16 tokens' sum times 2^(n - m) / s_v.
+// 2048 rows x 32 heads at 16384 tokens, d = 128: 598 us, 862 TFLOP/s; as a call 663 us.  No unit
+// is full: of about 4700 cycles that two row tiles take for 128 tokens, the products and the
+// exponentials take 2048 each and the issue slots half; the rest are waits of the roles for one
+// another, which two row tiles do not cover.  144, 128 and 96 registers, no spills (a spilled
+// value missed what is left of L1 and cost 600 cycles).
 constexpr int kTileThreads = 512, kTileMeta = 4, kItems = 8;
 struct __align__(16) TileMeta { float sk, lsv; int gone, pad; };   // 16 tokens: key scale, log2 of the value scale
 constexpr int kTileHalf = 128 * 128;                      // 128 rows of 64 fp16, 128-byte swizzle

@@ -278,6 +278,23 @@ def test_non_finite_values_are_seen(gpu, heads, kv, d, bs, new, lens, fmt, dtype
     assert sv.get_status() == sv.OK
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
+@pytest.mark.parametrize("fmt,dtype", BOTH_FORMATS)
+def test_a_nan_in_a_query_stays_in_its_row(gpu, heads, kv, d, bs, new, lens, fmt, dtype):
+    import torch
+    P, table = pool(sum(lens) + 7, heads, kv, d, bs, lens, fmt, dtype)
+    n = sum(new)
+    q = normal(P.rng, n, heads * d, dtype)
+    base, got, want, tol = both(P, q, new, lens, table, dtype=dtype)
+    within(got, want, tol)
+    q[n // 2, (heads - 1) * d + 3] = float("nan")
+    bits = both(P, q, new, lens, table, dtype=dtype)[0].view(n, heads, d)
+    assert torch.isnan(bits[n // 2, heads - 1].float()).all()
+    bits[n // 2, heads - 1] = base.view(n, heads, d)[n // 2, heads - 1]
+    assert torch.equal(bits, base.view(n, heads, d))
+
+
 # --------------------------------------------------------------- bad pages
 @pytest.mark.gpu
 @pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
