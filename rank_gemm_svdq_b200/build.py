@@ -29,24 +29,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(HERE, "..", "include", "svdq.h"),
                                                         os.path.abspath(__file__)]
-    objs = []
-    for src in SOURCES_CU:
+    objs, running = [], []                       # the sources are compiled at the same time
+    for src in SOURCES_CU + SOURCES_CPP:
         s = os.path.join(CSRC, src)
         o = os.path.join(BUILD, src + ".o")
-        if force or _stale(o, [s] + hdrs):
+        objs.append(o)
+        if not force and not _stale(o, [s] + hdrs):
+            continue
+        if src in SOURCES_CU:
             cmd = [NVCC, *ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                    "--expt-relaxed-constexpr", "-c", s, "-o", o]
             if verbose:
                 cmd.insert(1, "-Xptxas=-v")
-            subprocess.check_call(cmd)
-        objs.append(o)
-    for src in SOURCES_CPP:
-        s = os.path.join(CSRC, src)
-        o = os.path.join(BUILD, src + ".o")
-        if force or _stale(o, [s] + hdrs):
-            subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-fopenmp", "-ffp-contract=off",
-                                   "-c", s, "-o", o])
-        objs.append(o)
+        else:
+            cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fopenmp", "-ffp-contract=off", "-c", s, "-o", o]
+        running.append((cmd, o, subprocess.Popen(cmd)))
+    failed = [(cmd, o, p.returncode) for cmd, o, p in running if p.wait() != 0]
+    for cmd, o, _ in failed:
+        if os.path.exists(o):
+            os.remove(o)
+    if failed:
+        raise subprocess.CalledProcessError(failed[0][2], failed[0][0])
     if force or _stale(OUT, objs):
         tmp = OUT + f".{os.getpid()}.tmp"
         subprocess.check_call([NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static",
