@@ -329,19 +329,22 @@ __global__ void __launch_bounds__(append_threads(1 << LB, D), 768 / append_threa
   const int a = clampi(A.cu[i], 0, A.n_tokens), e = clampi(A.cu[i + 1], 0, A.n_tokens);
   if (a >= e) return;
   if (e - a > A.max_new && tid == 0) record_status(SVDQ_ERR_INVALID_ARG);
-  // o0: row of the request's first token in its block, from the first one that has a slot
+  // o0: row of the request's first token in its block.  Where that token has no slot, any other one tells: the first
+  // that has one among those that can be this item's (a longer search would make a long skipped prefix quadratic)
+  const int j = w - (a >> LB) - A.per * i;
   int lead = a, slot0 = A.slots[a];
   if (slot0 < 0) {
-    lead = first_with_slot<kAppendThreads>(A.slots, a, e);
-    if (lead == e) return;
+    const int to = (int)min((int64_t)e, a + (j + 1) * (int64_t)BS);
+    lead = first_with_slot<kAppendThreads>(A.slots, max(a, to - 2 * BS + 1), to);
+    if (lead >= to) return;
     slot0 = A.slots[lead];
   }
-  const int j = w - (a >> LB) - A.per * i, o0 = (slot0 - (lead - a)) & (BS - 1);
+  const int o0 = (slot0 - (lead - a)) & (BS - 1);
   const int64_t first = (int64_t)a + (j == 0 ? 0 : (int64_t)j * BS - o0);
   if (first >= e) return;
   // this item's tokens [t0, end), from the first one that has a slot
   int t0 = (int)first;
-  const int end = min(e, a + (j + 1) * BS - o0);
+  const int end = (int)min((int64_t)e, a + (j + 1) * (int64_t)BS - o0);
   slot0 = A.slots[t0];
   if (slot0 < 0) {
     t0 = first_with_slot<kAppendThreads>(A.slots, t0, end);

@@ -369,6 +369,26 @@ def test_append_leaves_skipped_tokens_out(gpu, fmt, d, bs, skip):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bs,d", [(16, 64), (128, 64), (128, 128)])
+def test_append_behind_a_long_skipped_prefix(gpu, bs, d):
+    """30000 tokens of which the first 29001 are cached already, and a request behind them."""
+    olds, news, skip = [7, 3], [30000, 50], 29001
+    lens = [a + b for a, b in zip(olds, news)]
+    P = Pool(bs, 1, 1, d, bs, sum(-(-L // bs) for L in lens) + 3, "int8", "bf16")
+    table = make_table(P.rng, lens, bs, P.n, max(-(-L // bs) for L in lens))
+    slots = [int(table[i, t // bs]) * bs + t % bs for i in (0, 1) for t in range(olds[i], lens[i])]
+    slots[:skip] = [-1] * skip
+    slots, cu = np.array(slots, np.int32), [0, news[0], sum(news)]
+    x = normal(P.rng, len(slots), d).to(dtype_of("bf16"))
+    want = appended(x.double().numpy().reshape(-1, 1, d), slots, cu, P.codes[0], P.scale[0], "int8")
+    c, xd = P.to_device(), x.cuda()
+    b = sv.paged_batch(dev(table), dev(np.array(lens, np.int32)), dev(np.array(cu, np.int32)), dev(slots), max_new=max(news), max_len=max(lens))
+    sv.paged_append(c, b, xd, xd)
+    assert np.array_equal(P.t[1].cpu().numpy(), want[1]) and np.array_equal(P.t[0].cpu().numpy(), want[0])
+    assert sv.get_status() == sv.OK
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("slots", [[0, 1, 3, 2], [3, 3, 5, 6], [0, 1, 34, 3], [5, 6, 7, 20], [-1, 4, 9, 6]])
 def test_append_records_tokens_astray(gpu, slots):
     """Slots of one request that do not follow one another in their block, the same slot twice, another block's slot:
