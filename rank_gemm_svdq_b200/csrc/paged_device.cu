@@ -1200,8 +1200,8 @@ struct FlatSmem {
 
 // CTAs an SM, which the schedule is sized by: four with 64 values a head and 8 rows; the accumulators of 16 rows, or
 // the ring of 128 values, leave three, both two.  The launch bounds hold the compiler to it, the assertion the ring.
-// 64 requests of up to 4096 tokens, 4 heads of 64 values, 16 query heads each: 47 us; with a grid for four CTAs an SM,
-// of which three fit, 53 us, and one request of 131071 tokens 48 instead of 35 us (graphs, warm L2).
+// 64 requests of up to 4096 tokens, 4 heads of 64 values, 16 query heads each: 47 us where a grid for four CTAs an SM, of
+// which three fit, took 53, and one request of 131071 tokens 35 instead of 48 (41.5 and 34 us now).
 constexpr int flat_per_sm(int head_dim, int rows) { return 4 - (head_dim > 64) - (rows > 8); }
 constexpr int kSmemPerSm = 228 * 1024, kSmemPerCta = 1024;   // what an SM has, and what it takes for itself for each CTA
 
