@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
 // where no request has more than one new token.  Bound by the chain lengths -> slots
 // -> rows of each CTA, so by how many CTAs are resident: at most 80 registers, 24 warps
 // an SM (at a time when a thread needed 80: 16 warps 25.8 us, 24 21.9, 32 with spills 22.4;
-// now 72 and no spills).  Five prompts of 15,000 tokens in all, 8 heads of 128: 21.7 us,
-// as a call 24.2 (3.6 TB/s); 48 single tokens 3.8 us, 1000 49 us (every CTA's search for
+// now 72 and no spills).  Five prompts of 15,000 tokens in all, 8 heads of 128: 21.9 us,
+// as a call 24.5 (3.6 TB/s); 48 single tokens 3.7 us, 1000 49 us (every CTA's search for
 // its request is linear in B).
 constexpr int append_threads(int BS, int D) { return BS * D >= 16384 ? 256 : 128; }
 
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(append_threads(1 << LB, D), 768 / append_threa
   if (first >= e) return;
   // this item's tokens [t0, end), from the first one that has a slot
   int t0 = (int)first;
-  const int end = (int)min((int64_t)e, a + (j + 1) * (int64_t)BS - o0);
+  const int end = t0 + min(e - t0, j == 0 ? BS - o0 : BS);
   slot0 = A.slots[t0];
   if (slot0 < 0) {
     t0 = first_with_slot<kAppendThreads>(A.slots, t0, end);
