@@ -140,8 +140,8 @@ def attend(q, cu, lens, table, kcodes, kscale, vcodes, vscale, fmt, causal, scal
       2^-23 (2 |log2 s_v| + |x|) E    the roundings of an exponent x + log2 s_v and of its terms (largest of each)
       T qmax F                        what is lost below fp16's normal numbers, half a step of 2^-24 for each of the T
                                       tokens that the row sees.  The step belongs to weights p s_v taken relative to a
-                                      reference at most twice the largest one that the row sees, so F = 2^-24 max p s_v;
-                                      2^-144 max p more where all s_v are below 2^-120 (the reference's lower end);
+                                      reference 2^6 below the largest one that the row sees, or lower, so F = 2^-31 max p s_v;
+                                      2^-144 max p more where all s_v are below 2^-113 (the reference's lower end);
                                       2^-119 max p max s_v for weights below the smallest fp32 number
     with dx = (d 2^-23) scale max_t sum |q| |k|: fp32 products added in any order, and q's own 2^-25."""
     n, heads, d = q.shape
@@ -169,7 +169,7 @@ def attend(q, cu, lens, table, kcodes, kscale, vcodes, vscale, fmt, causal, scal
             dx = d * 2.0 ** -23 * abs(scale) * (np.abs(q[a:e, h]) @ np.abs(k).T).max(axis=1, keepdims=True)
             sv = np.where(there, vscale[np.where(there, blocks, 0), h // G].astype(np.float64), 0.0)
             most = lambda w: np.max(np.where(seen, w, 0.0), axis=1, keepdims=True)  # noqa: E731
-            lost = 2.0 ** -24 * most(p * sv) + 2.0 ** -144 * most(p) + 2.0 ** -119 * most(p) * most(sv)
+            lost = 2.0 ** -31 * most(p * sv) + 2.0 ** -144 * most(p) + 2.0 ** -119 * most(p) * most(sv)
             far = 2 * most(np.abs(np.log2(np.where(sv > 0, sv, 1.0)))) + 1.45 * most(np.where(seen, np.abs(s), 0.0))
             tol[a:e, h] = unit * np.maximum(np.abs(out[a:e, h]), NORMAL[unit])
             tol[a:e, h] += (2.0 ** -11 + 2 * dx + 2.0 ** -19 + 2.0 ** -23 * far) * (p @ np.abs(v))

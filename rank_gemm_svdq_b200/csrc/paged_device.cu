@@ -462,12 +462,12 @@ __global__ void __launch_bounds__(append_threads(1 << LB, D), 768 / append_threa
 // exact up to 2^-25 of that entry, of 2^-120 for smaller ones); out = sum_t p_t s_v c^v_t / sum_t p_t, p_t = 2^(x_t - m).
 // Both products run on fp16 operands (8-bit codes are exact in fp16) with fp32
 // accumulators.  The sum takes p relative to m, a score seen so far; the product takes
-// p' = p s_v = 2^(x + log2 s_v - n), rounded to fp16, relative to n, a weighted
+// p' = p s_v = 2^(x + log2 s_v - n), rounded to fp16, relative to n, 2^kRoom below a weighted
 // magnitude x + log2 s_v seen so far.  Both come from what the row sees alone, so that
 // a large scale behind a causal mask, or of no weight, costs nothing.  Both may lag by 2^kGrow:
-// p' <= 2^7 does not overflow, what was summed is rarely rescaled, and a weight is
+// p' <= 2^14 does not overflow, what was summed is rarely rescaled, and a weight is
 // off by 2^-11 of itself (the size of the rounding of an fp16 output) or, below fp16's
-// normal numbers, by 2^-24 of the row's largest weighted magnitude.  At the end
+// normal numbers, by 2^-31 of the row's largest weighted magnitude.  At the end
 // O 2^(n - m) / l; pieces of rows are kept so divided and joined as means with the weights
 // 2^m l, which no sum of large values overflows.
 struct AttnArgs {
@@ -559,6 +559,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ int query_exponent(float top) { return clampi((int)(__float_as_uint(top) >> 23) - 127, -120, 113); }
 
 constexpr float kGrow = 7.0f;   // a softmax reference may lag by this much (2^7)
+// The largest weights are taken 2^kRoom above fp16's 1, so that many small ones keep as many more places.
+constexpr float kRoom = 7.0f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -566,10 +568,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// At least log2 s, at most one more; within [-120, 118], so that 2^(m - n) is a normal fp32 number.  A value scale
-// comes to 2^121 at most (the largest bf16 number over 127), and a weight so to 2^10.
+// At least log2 s, at most one more (122, of the largest bf16 number over 127); -113 for smaller s, so that 2^(m - n)
+// is a normal fp32 number.
 __device__ __forceinline__ float scale_exponent(float s) {
-  return fminf(fmaxf(__uint_as_float(0x4B000000u | (__float_as_uint(s) >> 23)) - 8388734.0f, -120.0f), 118.0f);   // 2^23 + field - (2^23 + 126)
+  return fmaxf(__uint_as_float(0x4B000000u | (__float_as_uint(s) >> 23)) - 8388734.0f, -113.0f);   // 2^23 + field - (2^23 + 126)
 }
 
 // A row's accumulator in units of 2^n to its result, 2^(n - m) / l, as two factors that neither over- nor underflow.
@@ -748,7 +750,7 @@ struct RowState {
         const float x0 = fmaxf(x[0][nb][i], x[0][nb][i + 2]) * fac[0][nb][i], x1 = fmaxf(x[1][nb][i], x[1][nb][i + 2]) * fac[1][nb][i];
         top[nb][i] = fmaxf(x0, x1);
         vtop[nb][i] = fmaxf(x0 + e0, x1 + e1);
-        grow = grow || top[nb][i] > m[nb][i] + kGrow || vtop[nb][i] > n[nb][i] + kGrow;
+        grow = grow || top[nb][i] > m[nb][i] + kGrow || vtop[nb][i] > n[nb][i] + (kGrow + kRoom);
       }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -766,9 +768,9 @@ struct RowState {
             m[nb][i] = top[nb][i];
           }
           b[i] = 1.0f;
-          if (vtop[nb][i] > n[nb][i] + kGrow) {
-            b[i] = ex2(n[nb][i] - vtop[nb][i]);
-            n[nb][i] = vtop[nb][i];
+          if (vtop[nb][i] > n[nb][i] + (kGrow + kRoom)) {
+            b[i] = ex2(n[nb][i] - (vtop[nb][i] - kRoom));
+            n[nb][i] = vtop[nb][i] - kRoom;
           }
         }
 #pragma unroll
@@ -781,7 +783,8 @@ struct RowState {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const float z0 = m[nb][0] == -INFINITY ? 0.0f : m[nb][0], z1 = m[nb][1] == -INFINITY ? 0.0f : m[nb][1];
-      // -125 <= m - n <= 127: n is at most a score (m + kGrow) plus 118; where m was set, n became at least m - 120 - kGrow
+      // -122 <= m - n <= 127: n is at most a score (m + kGrow) plus 122 - kRoom; where m was set, n became at least
+      // m - 113 - kGrow - kRoom
       const float rel0 = ex2(fminf(z0 - n[nb][0], 127.0f)), rel1 = ex2(fminf(z1 - n[nb][1], 127.0f));
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
@@ -1638,9 +1641,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
             vtop = fmaxf(vtop, x + lsv_of(g));             // of what the row sees: -inf elsewhere
           }
           // new references only where one grew by 2^kGrow (or is the first)
-          const bool grow = top > m + kGrow, vgrow = vtop > n + kGrow;   // -inf: any finite one
+          const bool grow = top > m + kGrow, vgrow = vtop > n + (kGrow + kRoom);   // -inf: any finite one
           if (__any_sync(0xffffffffu, grow || vgrow)) {
-            const float m1 = grow ? ceilf(top) : m, n1 = vgrow ? ceilf(vtop) : n;
+            const float m1 = grow ? ceilf(top) : m, n1 = vgrow ? ceilf(vtop) - kRoom : n;
             const float bo = n1 == n ? 1.0f : power_of_two(n - n1);
             l *= m1 == m ? 1.0f : power_of_two(m - m1);
             m = m1;

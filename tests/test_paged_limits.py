@@ -160,6 +160,25 @@ def test_large_values_of_no_weight(gpu, heads, kv, d, bs, new, lens, fmt, dtype,
     assert np.abs(got).max() < 1000
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
+@pytest.mark.parametrize("fmt,dtype", BOTH_FORMATS)
+def test_small_weights_of_many_tokens(gpu, heads, kv, d, bs, new, lens, fmt, dtype):
+    """The first token takes nearly all of the weight and has a value of 0: what is left are the others, at weights
+    of 2^-27 of its own and ordinary values."""
+    P, table = pool(sum(lens) + 8, heads, kv, d, bs, lens, fmt, dtype)
+    q = normal(P.rng, sum(new), heads * d, dtype) * 0 + 1
+    P.codes[0] = pk.to_codes(np.full((1,), 1.0), fmt)[0]
+    P.codes[0, table[:, 0], :, 0] = pk.to_codes(np.full((1,), 15.0), fmt)[0]
+    P.scale[0] = 27.0 * np.log(2.0) / 14.0 / d ** 0.5      # a step of 14 codes in all values is 27 in log2
+    P.codes[1, table[:, 0], :, 0] = 0
+    P.codes[1] = P.codes[1] & 0x7F if fmt == "e4m3" else np.abs(P.codes[1].view(np.int8)).view(np.uint8)
+    P.scale[1] = np.float32(256.0 if dtype == "fp16" else 1.0)
+    _, got, want, tol = both(P, q, new, lens, table, dtype=dtype)
+    within(got, want, tol)
+    assert (tol < 0.5 * np.abs(want)).mean() > 0.8         # the bound tells a lost tail from a kept one
+
+
 # ---------------------------------------------------- the smallest and the largest numbers
 @pytest.mark.gpu
 @pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
