@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
 // where no request has more than one new token.  Bound by the chain lengths -> slots
 // -> rows of each CTA, so by how many CTAs are resident: at most 80 registers, 24 warps
 // an SM (at a time when a thread needed 80: 16 warps 25.8 us, 24 21.9, 32 with spills 22.4;
-// now 72 and no spills).  Five prompts of 15,000 tokens in all, 8 heads of 128: 21.9 us,
-// as a call 24.5 (3.6 TB/s); 48 single tokens 3.7 us, 1000 49 us (every CTA's search for
+// now 72 and no spills).  Five prompts of 15,000 tokens in all, 8 heads of 128: 22.0 us,
+// as a call 24.8 (3.5 TB/s); 48 single tokens 3.7 us, 1000 49 us (every CTA's search for
 // its request is linear in B).
 constexpr int append_threads(int BS, int D) { return BS * D >= 16384 ? 256 : 128; }
 
@@ -1181,7 +1181,7 @@ struct Walk {
 // takes the 32 tokens at 32 w of each 128-token tile.  Pieces of cut items go to the
 // workspace for paged_join_kernel; where A.snap is set items are not cut, and belong to
 // the CTA in whose share they start.  64 requests of up to 4096 tokens (346 MB of int8
-// codes): 71.5 us, 4.8 TB/s; one of 131071 (268 MB of E4M3): 57 us.  Beyond HBM's rate it
+// codes): 71 us, 4.9 TB/s; one of 131071 (268 MB of E4M3): 57 us.  Beyond HBM's rate it
 // pays the first chain of loads, 5 us, queries and joins, and bank conflicts: value rows of
 // 128 bytes are read four lanes to a bank, key rows two, over a quarter of the kernel's cycles
 // by the counter.  Tiles of 16 tokens in 16 warps an SM instead of 32 in 12: 89 and 62 us
@@ -1395,7 +1395,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, flat_per_sm(D, 8 * NB)) paged_
 //   warp 13          walks the schedule, up to eight items ahead
 // The value scale goes into a weight's exponent, p' = 2^(x + log2 s_v - n), so it costs
 // nothing per weight; the row sum takes each 16 tokens' sum times 2^(n - m) / s_v.
-// 2048 rows x 32 heads at 16384 tokens, d = 128: 598 us, 862 TFLOP/s; as a call 663 us.  No unit
+// 2048 rows x 32 heads at 16384 tokens, d = 128: 598 us, 862 TFLOP/s; as a call 658 us.  No unit
 // is full: of about 4700 cycles that two row tiles take for 128 tokens, the products and the
 // exponentials take 2048 each and the issue slots half; the rest are waits of the roles for one
 // another, which two row tiles do not cover.  144, 128 and 96 registers, no spills (a spilled
