@@ -1392,7 +1392,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, flat_per_sm(D, 8 * NB)) paged_
 //                    by more than 2^7; the next item's queries; output
 //   warps 8-11       codes -> fp16 (the next tile's codes already in registers)
 //   warp 12          issues the MMAs: S0 S1 | P0V S0' | P1V S1' | ...
-//   warp 13          walks the schedule, up to eight items ahead
+//   warp 13          walks the schedule, up to eight items ahead; writes the zeros of
+//                    rows that see nothing.  Every item in the ring has a token tile: behind
+//                    eight without, the MMA warp would wait for an item that the softmax
+//                    warps hold back until it has served them
 // The value scale goes into a weight's exponent, p' = 2^(x + log2 s_v - n), so it costs
 // nothing per weight; the row sum takes each 16 tokens' sum times 2^(n - m) / s_v.
 // 2048 rows x 32 heads at 16384 tokens, d = 128: 598 us, 862 TFLOP/s; as a call 658 us.  No unit
@@ -1466,6 +1469,17 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
+}
+
+// Zeros for an item's rows, by one warp.
+template <int D>
+__device__ __forceinline__ void zero_rows(const AttnArgs& A, const Item& I) {
+  constexpr int PER = D / 8;
+  const int n = min(kTileRows, I.rows - I.r0) * PER;
+  for (int x = threadIdx.x & 31; x < n; x += 32) {
+    const int r = I.r0 + x / PER;
+    *reinterpret_cast<uint4*>(A.out + (int64_t)(I.a + r / A.G) * A.out_stride + (int64_t)(I.h * A.G + r % A.G) * D + 8 * (x % PER)) = make_uint4(0, 0, 0, 0);
+  }
 }
 
 template <int DT, int FMT, int D>
@@ -1756,13 +1770,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
     Next nxt;
     const auto advance = [&](Next& N) {                    // one token tile on: false after the last
       if (++j >= hi) {
-        do {
-          if (k >= 0) give_back(k);
-          if (!take(++k)) return false;
-          j = items[k % kItems].lo;
-          hi = items[k % kItems].hi;
-        } while (hi <= j);
+        if (k >= 0) give_back(k);
+        if (!take(++k)) return false;
         const Item& I = items[k % kItems];
+        j = I.lo;
+        hi = I.hi;
         h = I.h;
         nblk = blocks_of(I.L, A.lb);
         row = A.table + (size_t)I.req * A.max_blocks;
@@ -1848,12 +1860,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
     int k = 0;
     const auto advance = [&](Tile& T) {
       if (++T.j < T.hi) return true;
-      do {
-        if (!take(k)) return false;
-        const Item& I = items[k % kItems];
-        T = Tile{I.lo, I.lo, I.hi, I.end[0], I.end[1]};
-        give_back(k++);
-      } while (T.hi <= T.lo);
+      if (!take(k)) return false;
+      const Item& I = items[k % kItems];
+      T = Tile{I.lo, I.lo, I.hi, I.end[0], I.end[1]};
+      give_back(k++);
       return true;
     };
     const auto issue_s = [&](int rt, int st) {
@@ -1945,7 +1955,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tiles_kernel(const Attn
     if (left) walk.start(A, share, kTileRows);
     for (int k = 0;; ++k) {
       Item I;
-      left = left && walk.next(A, share, kTileRows, I);
+      while ((left = left && walk.next(A, share, kTileRows, I)) && I.hi <= I.lo) zero_rows<D>(A, I);
       if (!left) I.hi = -1;
       if (k >= kItems && !mbar_wait(&i_empty[k % kItems], (k / kItems - 1) & 1, &s_abort)) break;
       if (lane == 0) {

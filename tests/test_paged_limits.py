@@ -258,6 +258,22 @@ def test_append_keeps_the_sign_of_zero(gpu, fmt, size):
     assert np.array_equal(P.t[0].cpu().numpy(), want[0]) and np.array_equal(P.t[1].cpu().numpy(), want[1])
 
 
+# ------------------------------------------------------ rows that see nothing
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,d,bs,new,lens", [
+    (64, 8, 128, 16, [1500] * 6, [20, 0, 1, 140, 7, 3]), (24, 8, 64, 64, [700] * 12, [0, 0, 50, 0, 0, 300, 0, 0, 0, 0, 0, 1]),
+    (160, 8, 128, 128, [300, 17, 250] * 6, [20, 3, 11] * 6), (8, 8, 64, 16, [5000, 1, 5000], [0, 9, 0])])
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_rows_that_see_nothing(gpu, heads, kv, d, bs, new, lens, causal):
+    """Hundreds of 256-row items without a token in between others: zeros, and nobody waits."""
+    P, table = pool(sum(lens) + 9, heads, kv, d, bs, lens, "int8", "bf16")
+    _, got, want, tol = both(P, normal(P.rng, sum(new), heads * d), new, lens, table, causal)
+    within(got, want, tol)
+    assert sv.get_status() == sv.OK
+    if causal or 0 in lens:                                # otherwise every row sees something
+        assert (want == 0).all(axis=2).any()
+
+
 # ------------------------------------------------------- NaN and infinities
 @pytest.mark.gpu
 @pytest.mark.parametrize("heads,kv,d,bs,new,lens", PATHS)
